@@ -22,10 +22,12 @@ __all__ = [
     "kalm_merged_attention_out_proj", "kalm_merged_attention_out_proj_static", "kalm_attention_out_proj_sync_len",
     "kalm_yes_no_score", "kalm_broadcast_rows", "kalm_selftest_wait_timeout", "kalm_attention_items",
     "kalm_attention_schedule", "kalm_rope", "kalm_rope_table", "kalm_linear_rope",
+    "kalm_cache_write", "kalm_cache_read", "kalm_merged_attention_cache", "kalm_rms_norm", "kalm_norm_residual",
 ]
 
 HEAD_DIM = 256
 MAX_QUERY_TOKENS = 512  # KALM_MAX_QUERY_TOKENS
+CACHE_GROUP = 32  # KALM_CACHE_GROUP: columns of a cached row that share a scale
 
 
 def _stream(stream: Optional[torch.cuda.Stream]) -> int:
@@ -48,6 +50,34 @@ def _ld(t: torch.Tensor) -> int:
     if t.dim() != 2 or t.stride(1) != 1:
         raise KalmError(1, "binding", "expected a 2-D tensor with contiguous rows")
     return t.stride(0)
+
+
+def _check(where: str, dtype: torch.dtype, *tensors: Optional[torch.Tensor]) -> None:
+    """Tensors of one type on the current device (None passes)."""
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise KalmError(1, where, "tensors must live on the CUDA device")
+        if t.dtype != dtype:
+            raise KalmError(1, where, f"expected {dtype}, got {t.dtype}")
+        if t.get_device() != torch.cuda.current_device():
+            raise KalmError(1, where, f"tensor on {t.device}, current device is cuda:{torch.cuda.current_device()}")
+
+
+def _rows(where: str, name: str, t: torch.Tensor, rows: Optional[int] = None, width: Optional[int] = None) -> int:
+    """Row stride (elements) of a 2-D view with contiguous rows, after checking its sizes."""
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1):
+        raise KalmError(1, where, f"{name}: expected a 2-D tensor with contiguous rows")
+    if (rows is not None and t.shape[0] != rows) or (width is not None and t.shape[1] != width):
+        raise KalmError(1, where, f"{name} has shape {tuple(t.shape)}, expected ({rows}, {width})")
+    # the stride of a single row is arbitrary in torch; any that covers the row will do
+    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 16) * 16
+
+
+def _vector(where: str, name: str, t: Optional[torch.Tensor], n: int) -> None:
+    if t is not None and (t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1)):
+        raise KalmError(1, where, f"{name}: expected a contiguous vector of {n}")
 
 
 def kalm_version() -> int:
@@ -270,6 +300,154 @@ def kalm_linear_rope(x: torch.Tensor, w: torch.Tensor, y: torch.Tensor, q_off: t
     call("kalm_linear_rope", _p(x, torch.bfloat16), _ld(x), _p(w, torch.bfloat16), _ld(w), _p(y, torch.bfloat16),
          _ld(y), m, n, k, rot_heads * head_dim, head_dim, _p(q_off, torch.int64), q_off.numel() - 1,
          _p(table, torch.float32), _stream(stream))
+
+
+def _cache_args(where: str, row_off: torch.Tensor, page_table: torch.Tensor, page_rows: int, codes: torch.Tensor,
+                scales: torch.Tensor, width: int, first_row: Optional[torch.Tensor] = None):
+    """Checks what the calls on a document cache share; (n_docs, ld_table, n_pages, ld_codes, ld_scales)."""
+    _check(where, torch.int64, row_off)
+    _check(where, torch.int32, page_table, first_row)
+    _check(where, torch.uint8, codes, scales)
+    n_docs = row_off.numel() - 1
+    if n_docs < 0:
+        raise KalmError(1, where, "the offsets are empty")
+    _vector(where, "offsets", row_off, n_docs + 1)
+    _vector(where, "first_row", first_row, n_docs)
+    if page_table.dim() != 2 or page_table.shape[0] != n_docs or not page_table.is_contiguous():
+        raise KalmError(1, where, f"page_table: expected a contiguous [{n_docs}][pages] tensor")
+    if page_rows <= 0 or codes.shape[0] % page_rows:
+        raise KalmError(1, where, f"{codes.shape[0]} cache rows are not whole pages of {page_rows}")
+    ld_codes = _rows(where, "codes", codes, None, width)
+    ld_scales = _rows(where, "scales", scales, codes.shape[0], width // CACHE_GROUP)
+    return n_docs, page_table.shape[1], codes.shape[0] // page_rows, ld_codes, ld_scales
+
+
+def kalm_cache_write(src: torch.Tensor, row_off: torch.Tensor, page_table: torch.Tensor, page_rows: int,
+                     codes: torch.Tensor, scales: torch.Tensor, first_row: Optional[torch.Tensor] = None,
+                     stream=None) -> None:
+    """Quantise packed bf16 rows into the pages of an 8-bit document cache.
+
+    src [rows][width]: document d's rows are row_off[d] .. row_off[d+1] - 1 and become rows
+    first_row[d] .. of the document (first_row None: from its row 0).  page_table int32
+    [n_docs][pages]; codes uint8 [n_pages * page_rows][width]; scales uint8 [same rows][width / 32].
+    No two rows may have the same place."""
+    where = "kalm_cache_write"
+    _check(where, torch.bfloat16, src)
+    ld_src = _rows(where, "src", src)
+    n_docs, ld_table, n_pages, ld_codes, ld_scales = _cache_args(where, row_off, page_table, page_rows, codes, scales,
+                                                                 src.shape[1], first_row)
+    call(where, src.data_ptr(), ld_src, row_off.data_ptr(), n_docs, src.shape[0], src.shape[1],
+         None if first_row is None else first_row.data_ptr(), page_table.data_ptr(), ld_table, page_rows, n_pages,
+         codes.data_ptr(), ld_codes, scales.data_ptr(), ld_scales, _stream(stream))
+
+
+def kalm_cache_read(codes: torch.Tensor, scales: torch.Tensor, row_off: torch.Tensor, page_table: torch.Tensor,
+                    page_rows: int, dst: torch.Tensor, first_row: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Read cached rows back into packed bf16 rows: dst[row_off[d] + i] = row first_row[d] + i of
+    document d (the stored values exactly).  Arguments as kalm_cache_write."""
+    where = "kalm_cache_read"
+    _check(where, torch.bfloat16, dst)
+    ld_dst = _rows(where, "dst", dst)
+    n_docs, ld_table, n_pages, ld_codes, ld_scales = _cache_args(where, row_off, page_table, page_rows, codes, scales,
+                                                                 dst.shape[1], first_row)
+    call(where, codes.data_ptr(), ld_codes, scales.data_ptr(), ld_scales, row_off.data_ptr(), n_docs, dst.shape[0],
+         dst.shape[1], None if first_row is None else first_row.data_ptr(), page_table.data_ptr(), ld_table, page_rows,
+         n_pages, dst.data_ptr(), ld_dst, _stream(stream))
+
+
+def kalm_merged_attention_cache(q: torch.Tensor, k_self: torch.Tensor, v_self: torch.Tensor, k_codes: torch.Tensor,
+                                k_scales: torch.Tensor, v_codes: torch.Tensor, v_scales: torch.Tensor,
+                                page_table: torch.Tensor, page_rows: int, q_off: torch.Tensor, pool_off: torch.Tensor,
+                                max_q: int, n_q: int, n_kv: int, out: torch.Tensor, scale: Optional[float] = None,
+                                lse: Optional[torch.Tensor] = None, head_dim: int = HEAD_DIM,
+                                in_off: Optional[torch.Tensor] = None, last_tile_only: bool = False,
+                                total_q: Optional[int] = None, order: Optional[torch.Tensor] = None,
+                                stream=None) -> None:
+    """kalm_merged_attention with the cross K/V of an 8-bit document cache: document d attends to its
+    first pool_off[d+1] - pool_off[d] cached rows.  k/v codes uint8 [cache rows][n_kv * head_dim]
+    (column views of the cached rows are fine), k/v scales uint8 [cache rows][n_kv * head_dim / 32];
+    the other arguments as kalm_merged_attention."""
+    where = "kalm_merged_attention_cache"
+    if scale is None:
+        scale = head_dim ** -0.5
+    _check(where, torch.bfloat16, q, k_self, v_self, out)
+    _check(where, torch.int64, q_off, in_off)
+    _check(where, torch.int32, order)
+    _check(where, torch.float32, lse)
+    n_docs, ld_table, n_pages, ld_codes, ld_scales = _cache_args(where, pool_off, page_table, page_rows, k_codes,
+                                                                 k_scales, n_kv * head_dim)
+    _check(where, torch.uint8, v_codes, v_scales)
+    rows, cached = q.shape[0], k_codes.shape[0]
+    if _rows(where, "v_codes", v_codes, cached, n_kv * head_dim) != ld_codes or \
+            _rows(where, "v_scales", v_scales, cached, n_kv * head_dim // CACHE_GROUP) != ld_scales:
+        raise KalmError(1, where, "the cached K and V must share their row strides")
+    ld_self = _rows(where, "k_self", k_self, rows, n_kv * head_dim)
+    if _rows(where, "v_self", v_self, rows, n_kv * head_dim) != ld_self:
+        raise KalmError(1, where, "K and V views must share a row stride")
+    ldq = _rows(where, "q", q, rows, n_q * head_dim)
+    ldo = _rows(where, "out", out, None, n_q * head_dim)
+    _vector(where, "q_off", q_off, n_docs + 1)
+    _vector(where, "in_off", in_off, n_docs)
+    total_q = out.shape[0] if total_q is None else total_q
+    if total_q > out.shape[0] or (in_off is None and total_q > rows):
+        raise KalmError(1, where, f"total_q={total_q} exceeds the rows of out ({out.shape[0]}) or q ({rows})")
+    if lse is not None and (not lse.is_contiguous() or lse.dim() != 2 or lse.shape[0] < total_q or lse.shape[1] != n_q):
+        raise KalmError(1, where, f"lse: expected a contiguous [{total_q}][{n_q}] tensor")
+    if order is not None and order.numel() < kalm_attention_items(n_docs, max_q, n_q, n_kv, last_tile_only):
+        raise KalmError(1, where, "order is shorter than the call's work items")
+    call(where, q.data_ptr(), ldq, k_self.data_ptr(), v_self.data_ptr(), ld_self, k_codes.data_ptr(),
+         v_codes.data_ptr(), ld_codes, k_scales.data_ptr(), v_scales.data_ptr(), ld_scales, page_table.data_ptr(),
+         ld_table, page_rows, n_pages, q_off.data_ptr(), None if in_off is None else in_off.data_ptr(), rows,
+         pool_off.data_ptr(), n_docs, int(max_q), int(total_q), n_q, n_kv, head_dim, float(scale),
+         1 if last_tile_only else 0, None if order is None else order.data_ptr(), out.data_ptr(), ldo,
+         None if lse is None else lse.data_ptr(), _stream(stream))
+
+
+def kalm_rms_norm(x: torch.Tensor, w: torch.Tensor, h: torch.Tensor, eps: float = 1e-6, weight_offset: float = 0.0,
+                  stream=None) -> None:
+    """h = x / sqrt(mean(x^2) + eps) * (w + weight_offset), row by row; h may be x."""
+    where = "kalm_rms_norm"
+    _check(where, torch.bfloat16, x, w, h)
+    rows, width = x.shape
+    _vector(where, "w", w, width)
+    call(where, x.data_ptr(), _rows(where, "x", x), w.data_ptr(), h.data_ptr(), _rows(where, "h", h, rows, width), rows,
+         width, eps, weight_offset, _stream(stream))
+
+
+def kalm_norm_residual(y: torch.Tensor, x: torch.Tensor, x_out: torch.Tensor, h: Optional[torch.Tensor] = None,
+                       w_post: Optional[torch.Tensor] = None, w_pre: Optional[torch.Tensor] = None,
+                       gate: Optional[torch.Tensor] = None, q_off: Optional[torch.Tensor] = None,
+                       residual_scale: float = 1.0, eps: float = 1e-6, weight_offset: float = 0.0,
+                       stream=None) -> None:
+    """Between two blocks: t = residual_scale * x + gate * norm(y, w_post), x_out = t, h = norm(t, w_pre).
+
+    gate: None, one vector [width], or one per document [n_docs][width] (with q_off, the documents'
+    row offsets).  With q_off only the documents' rows are computed.  w_post None: y enters without a
+    norm; h and w_pre go together.  x_out may be x."""
+    where = "kalm_norm_residual"
+    _check(where, torch.bfloat16, y, x, x_out, h, w_post, w_pre, gate)
+    _check(where, torch.int64, q_off)
+    rows, width = x.shape
+    _vector(where, "w_post", w_post, width)
+    _vector(where, "w_pre", w_pre, width)
+    n_docs = 0 if q_off is None else q_off.numel() - 1
+    if n_docs < 0:
+        raise KalmError(1, where, "the offsets are empty")
+    if q_off is not None:
+        _vector(where, "q_off", q_off, n_docs + 1)
+    ld_gate = 0
+    if gate is not None:
+        if gate.dim() == 2:
+            if q_off is None:
+                raise KalmError(1, where, "a gate per document needs q_off")
+            ld_gate = _rows(where, "gate", gate, n_docs, width)
+        else:
+            _vector(where, "gate", gate, width)
+    p = lambda t: None if t is None else t.data_ptr()
+    call(where, y.data_ptr(), _rows(where, "y", y, rows, width), x.data_ptr(), _rows(where, "x", x), p(w_post), p(gate),
+         ld_gate, p(q_off), n_docs, residual_scale, x_out.data_ptr(), _rows(where, "x_out", x_out, rows, width),
+         p(w_pre), p(h), 0 if h is None else _rows(where, "h", h, rows, width), rows, width, eps, weight_offset,
+         _stream(stream))
 
 
 def kalm_selftest_wait_timeout(wait_ns: int, stream=None) -> None:

@@ -1,0 +1,284 @@
+// The 8-bit document cache: rows of bf16 vectors (pooled passage vectors, or their cross K/V) quantised into
+// pages as they are written, and read back.  "KaLM-Reranker-V1-Nano - MLX (Apple Silicon)", "What this is": a
+// passage's pooled vectors are computed once and cached for later queries; the pages name no storage type
+// for them, e4m3 with power-of-two scales is this library's.
+//
+// For each 32 consecutive columns of a row, with t = max |v| over the finite values:
+//   e = the least integer with t <= 448 * 2^e, at least -120      (448 = the largest e4m3 number)
+//   code = v * 2^-e rounded to nearest even                       (at most 240 where e = 120)
+// The product with 2^-e is exact, so a value is rounded once, by at most 2^-4 of itself (half a step of a
+// 3-bit mantissa; 2^-10 * 2^e where it is below the normal range).
+//
+// Both kernels stream: bound by HBM, 3 + 1/32 bytes a value.  A lane takes 8 columns (16 bytes of bf16, 8 bytes
+// of codes), so a warp's loads and stores are runs of whole lines on both sides and four neighbouring lanes
+// hold one scale group; kUnits such slices per lane are loaded before the first is used.  A warp's units are
+// consecutive, so it searches the document of its first row once (32 offsets a round) and walks on from there.
+#include "kalm.h"
+#include "kalm_cache.cuh"
+#include "kalm_internal.h"
+#include "kalm_ptx.cuh"
+
+namespace kalm {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnits = 4;  // 8-column slices a lane keeps in flight
+
+// The document that holds packed row r: the largest d with off[d] <= r (0 if none).  A warp searches together.
+__device__ __forceinline__ int find_doc_warp(const int64_t* __restrict__ off, int n_docs, int64_t r, int lane) {
+  int lo = 0, hi = n_docs;  // off[lo] <= r < off[hi], taking off[0] <= r
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + step * (lane + 1);
+    const unsigned below = __ballot_sync(0xffffffffu, at < hi && __ldg(off + at) <= r);
+    const int n = __popc(below);
+    hi = min(hi, lo + step * (n + 1));
+    lo += step * n;
+  }
+  return lo;
+}
+
+struct Rows {
+  const int64_t* off;    // [n_docs + 1] packed rows of each document
+  const int32_t* first;  // [n_docs] row of the document that its first packed row becomes, or NULL: 0
+  int n_docs;
+  int64_t total;         // packed rows in memory; those from off[n_docs] on belong to no document
+  int upr;               // 8-column units of a row
+};
+
+// A lane's units: their packed rows and columns, and the cache rows they belong to (-1: none).
+struct Unit {
+  int64_t row, at;
+  int col;
+};
+
+__device__ __forceinline__ void locate(Unit (&u)[kUnits], const Rows& rows, const CachePages& pages, uint32_t* err) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
+  const int64_t base = warp * 32 * kUnits;
+  const int64_t r0 = base / rows.upr;
+  const int c0 = static_cast<int>(base - r0 * rows.upr);
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) u[i].at = -1;
+  if (r0 >= rows.total) return;
+  int d = find_doc_warp(rows.off, rows.n_docs, r0, lane);
+  int64_t begin = __ldg(rows.off + d), end = __ldg(rows.off + d + 1);
+  int64_t r = r0;
+  int64_t held = -1, held_at = -1;  // the last row looked up
+  int c = c0 + lane;
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i, c += 32) {
+    while (c >= rows.upr) {
+      c -= rows.upr;
+      ++r;
+    }
+    u[i].row = r;
+    u[i].col = c;
+    if (r != held) {
+      while (r >= end && d + 1 < rows.n_docs) {  // a later document's row (skips empty ones)
+        ++d;
+        begin = end;
+        end = __ldg(rows.off + d + 1);
+      }
+      held = r;
+      held_at = -1;
+      if (r < rows.total && r >= begin && r < end) {
+        const int64_t i_doc = r - begin + (rows.first ? __ldg(rows.first + d) : 0);
+        held_at = i_doc >= 0 ? cache_row(pages, d, i_doc) : -1;
+        if (held_at < 0) record_error(err, kErrDeviceArg | kSiteCache);
+      }
+    }
+    u[i].at = held_at;
+  }
+}
+
+// Scale exponent of a group whose largest finite magnitude has these bf16 bits (without the sign).
+__device__ __forceinline__ int group_exp(uint32_t top) {
+  // top = 1.m * 2^k with k = (top >> 7) - 127; 448 = 1.75 * 2^8, and 1.75 is m = 0x60.  Zero and bf16's
+  // subnormals come out below the least exponent.
+  const int e = static_cast<int>(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0);
+  return max(e, kCacheMinExp);
+}
+
+__global__ void __launch_bounds__(kThreads) cache_write_kernel(const uint4* __restrict__ src, int64_t ld_src_v,
+                                                               const Rows rows, const CachePages pages,
+                                                               uint8_t* __restrict__ codes, int64_t ld_codes,
+                                                               uint8_t* __restrict__ scales, int64_t ld_scales,
+                                                               uint32_t* err) {
+  pdl_launch_dependents();
+  pdl_wait_predecessor();
+  Unit u[kUnits];
+  locate(u, rows, pages, err);
+  uint4 x[kUnits];
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    x[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (u[i].at >= 0) x[i] = __ldg(src + u[i].row * ld_src_v + u[i].col);
+  }
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    // largest magnitude: bf16 magnitudes order as their bits do
+    uint32_t m2 = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m2 = __vmaxu2(m2, w[k] & 0x7fff7fffu);
+    uint32_t top = max(m2 & 0xffffu, m2 >> 16);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const bool odd = top >= 0x7f80u;  // an infinity or NaN in the group: the scale is the finite values'
+    if (odd) {
+      top = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t b = (w[k >> 1] >> (16 * (k & 1))) & 0x7fffu;
+        if (b < 0x7f80u) top = max(top, b);
+      }
+    }
+    if (__any_sync(0xffffffffu, odd)) {
+      uint32_t o = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      o = max(o, __shfl_xor_sync(0xffffffffu, o, 2));
+      if (odd) top = o;
+    }
+    const int e = group_exp(top);
+    const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    const float lim = e >= kCacheMaxExp ? 240.f : 448.f;
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = __uint_as_float(w[k] << 16) * inv;
+      v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u) * inv;
+    }
+    if (odd || e >= kCacheMaxExp) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t b = (w[k >> 1] >> (16 * (k & 1))) & 0x7fffu;
+        // an infinity is stored as NaN: no finite code may stand for it
+        v[k] = b >= 0x7f80u ? __uint_as_float(0x7fffffffu) : fminf(fmaxf(v[k], -lim), lim);
+      }
+    }
+    uint2 out;
+    uint32_t* o = &out.x;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * k], v[2 * k + 1]), __NV_SATFINITE, __NV_E4M3);
+      if (k & 1)
+        o[k >> 1] |= two << 16;
+      else
+        o[k >> 1] = two;
+    }
+    if (u[i].at >= 0) {
+      *reinterpret_cast<uint2*>(codes + u[i].at * ld_codes + u[i].col * 8) = out;
+      if ((u[i].col & 3) == 0) scales[u[i].at * ld_scales + (u[i].col >> 2)] = static_cast<uint8_t>(e + 127);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const uint8_t* __restrict__ codes, int64_t ld_codes,
+                                                              const uint8_t* __restrict__ scales, int64_t ld_scales,
+                                                              const Rows rows, const CachePages pages,
+                                                              uint4* __restrict__ dst, int64_t ld_dst_v,
+                                                              uint32_t* err) {
+  pdl_launch_dependents();
+  pdl_wait_predecessor();
+  Unit u[kUnits];
+  locate(u, rows, pages, err);
+  uint2 x[kUnits];
+  uint32_t s[kUnits];
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i)
+    if (u[i].at >= 0) {
+      x[i] = __ldg(reinterpret_cast<const uint2*>(codes + u[i].at * ld_codes + u[i].col * 8));
+      s[i] = __ldg(scales + u[i].at * ld_scales + (u[i].col >> 2));
+    }
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i)
+    if (u[i].at >= 0) {
+      const uint32_t s2 = scale_bf16x2(s[i]);
+      const uint2 a = e4m3x4_scaled(x[i].x, s2), b = e4m3x4_scaled(x[i].y, s2);
+      dst[u[i].row * ld_dst_v + u[i].col] = make_uint4(a.x, a.y, b.x, b.y);
+    }
+}
+
+}  // namespace
+}  // namespace kalm
+
+using namespace kalm;
+
+namespace {
+
+// What the two calls check alike.  `bf` is the bf16 side.
+kalm_status check_cache_args(const char* what, const void* bf, int64_t ld_bf, const int64_t* row_off, int32_t n_docs,
+                             int64_t total_rows, int32_t width, const int32_t* page_table, int64_t ld_table,
+                             int32_t page_rows, int64_t n_pages, const uint8_t* codes, int64_t ld_codes,
+                             const uint8_t* scales, int64_t ld_scales) {
+  if (n_docs < 0 || total_rows < 0 || width <= 0 || width % kCacheGroup)
+    return fail(KALM_ERR_INVALID_ARG, "%s: n_docs=%d total_rows=%lld width=%d (a positive multiple of 32)", what,
+                n_docs, (long long)total_rows, width);
+  if (page_rows < KALM_CACHE_MIN_PAGE_ROWS || page_rows > KALM_CACHE_MAX_PAGE_ROWS || (page_rows & (page_rows - 1)))
+    return fail(KALM_ERR_INVALID_ARG, "%s: page_rows=%d is not a power of two in [%d, %d]", what, page_rows,
+                KALM_CACHE_MIN_PAGE_ROWS, KALM_CACHE_MAX_PAGE_ROWS);
+  if (n_pages < 0 || n_pages > INT32_MAX || ld_table < 0)
+    return fail(KALM_ERR_INVALID_ARG, "%s: n_pages=%lld ld_table=%lld", what, (long long)n_pages, (long long)ld_table);
+  if (ld_bf % 8 || ld_bf < width || ld_codes % 16 || ld_codes < width || ld_scales < width / kCacheGroup)
+    return fail(KALM_ERR_INVALID_ARG, "%s: row strides %lld (values), %lld (codes), %lld (scales) for width %d", what,
+                (long long)ld_bf, (long long)ld_codes, (long long)ld_scales, width);
+  if (n_docs == 0 || total_rows == 0) return KALM_OK;
+  if (!bf || !row_off || !page_table || !codes || !scales)
+    return fail(KALM_ERR_INVALID_ARG, "%s: NULL pointer", what);
+  if (!aligned16(bf) || !aligned16(codes))
+    return fail(KALM_ERR_INVALID_ARG, "%s: values and codes must be 16-byte aligned", what);
+  if ((total_rows * static_cast<__int128>(width) / 8 + 32 * kUnits) / (kThreads * kUnits) > INT32_MAX - 1)
+    return fail(KALM_ERR_INVALID_ARG, "%s: too many values (%lld rows of %d)", what, (long long)total_rows, width);
+  return KALM_OK;
+}
+
+Rows make_rows(const int64_t* row_off, const int32_t* first_row, int32_t n_docs, int64_t total_rows, int32_t width) {
+  return Rows{row_off, first_row, n_docs, total_rows, width / 8};
+}
+
+CachePages make_pages(const int32_t* page_table, int64_t ld_table, int32_t page_rows, int64_t n_pages) {
+  return CachePages{page_table, ld_table, n_pages, __builtin_ctz(static_cast<unsigned>(page_rows))};
+}
+
+dim3 cache_grid(int64_t total_rows, int32_t width) {
+  const int64_t units = total_rows * (width / 8);
+  return dim3(static_cast<unsigned>((units + kThreads * kUnits - 1) / (kThreads * kUnits)));
+}
+
+}  // namespace
+
+extern "C" kalm_status kalm_cache_write(const kalm_bf16* src, int64_t ld_src, const int64_t* row_off, int32_t n_docs,
+                                        int64_t total_rows, int32_t width, const int32_t* first_row,
+                                        const int32_t* page_table, int64_t ld_table, int32_t page_rows,
+                                        int64_t n_pages, uint8_t* codes, int64_t ld_codes, uint8_t* scales,
+                                        int64_t ld_scales, kalm_stream_t stream) {
+  kalm_status st = check_cache_args("kalm_cache_write", src, ld_src, row_off, n_docs, total_rows, width, page_table,
+                                    ld_table, page_rows, n_pages, codes, ld_codes, scales, ld_scales);
+  if (st != KALM_OK) return st;
+  if ((st = ensure_device(nullptr)) != KALM_OK) return st;
+  if (n_docs == 0 || total_rows == 0) return KALM_OK;
+  return check_cuda(launch_pdl(cache_write_kernel, cache_grid(total_rows, width), dim3(kThreads), 0,
+                               static_cast<cudaStream_t>(stream), reinterpret_cast<const uint4*>(src), ld_src / 8,
+                               make_rows(row_off, first_row, n_docs, total_rows, width),
+                               make_pages(page_table, ld_table, page_rows, n_pages), codes, ld_codes, scales,
+                               ld_scales, device_error_word()),
+                    "launch cache_write_kernel");
+}
+
+extern "C" kalm_status kalm_cache_read(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales,
+                                       int64_t ld_scales, const int64_t* row_off, int32_t n_docs, int64_t total_rows,
+                                       int32_t width, const int32_t* first_row, const int32_t* page_table,
+                                       int64_t ld_table, int32_t page_rows, int64_t n_pages, kalm_bf16* dst,
+                                       int64_t ld_dst, kalm_stream_t stream) {
+  kalm_status st = check_cache_args("kalm_cache_read", dst, ld_dst, row_off, n_docs, total_rows, width, page_table,
+                                    ld_table, page_rows, n_pages, codes, ld_codes, scales, ld_scales);
+  if (st != KALM_OK) return st;
+  if ((st = ensure_device(nullptr)) != KALM_OK) return st;
+  if (n_docs == 0 || total_rows == 0) return KALM_OK;
+  return check_cuda(launch_pdl(cache_read_kernel, cache_grid(total_rows, width), dim3(kThreads), 0,
+                               static_cast<cudaStream_t>(stream), codes, ld_codes, scales, ld_scales,
+                               make_rows(row_off, first_row, n_docs, total_rows, width),
+                               make_pages(page_table, ld_table, page_rows, n_pages), reinterpret_cast<uint4*>(dst),
+                               ld_dst / 8, device_error_word()),
+                    "launch cache_read_kernel");
+}

@@ -87,7 +87,8 @@ kalm_status kalm_device_check(void);
  * one, let every stream that runs library kernels go idle first).
  * *word_out (nullable) receives the raw word: bit 0 = a bounded wait expired,
  * bit 1 = invalid device data (e.g. a length above its limit); bits 8..15 name
- * the kernel (1 pool, 2 linear, 3 attention, 4 readout, 5 offsets, 6 self-test).
+ * the kernel (1 pool, 2 linear, 3 attention, 4 readout, 5 offsets, 6 self-test,
+ * 7 rotary embedding, 8 document cache).
  * Returns KALM_ERR_TIMEOUT, KALM_ERR_DEVICE_ARG or KALM_OK. */
 kalm_status kalm_check_device_errors(kalm_stream_t stream, uint32_t* word_out);
 
@@ -454,6 +455,128 @@ kalm_status kalm_rope_table(float theta, int32_t head_dim, float* table, kalm_st
 kalm_status kalm_linear_rope(const kalm_bf16* x, int64_t ldx, const kalm_bf16* w, int64_t ldw, kalm_bf16* y,
                              int64_t ldy, int64_t m, int32_t n, int32_t k, int32_t rot_cols, int32_t head_dim,
                              const int64_t* q_off, int32_t n_docs, const float* table, kalm_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The 8-bit document cache.
+ * "KaLM-Reranker-V1-Nano - MLX (Apple Silicon)", "What this is": each passage is
+ * encoded and pooled once, and later queries read its cached vectors; the pages
+ * name no storage type.  Here: rows of bf16 values (pooled vectors, or their cross
+ * K/V of every layer, in kalm_cross_kv_proj's layout) stored as 8-bit codes in
+ * pages, so that documents come and go one by one and a query names any of them.
+ *
+ * Numbers.  A cached row holds one e4m3 code per column (1 sign, 4 exponent and
+ * 3 mantissa bits, bias 7, largest 448, no infinity; 0x7f and 0xff are NaN) and
+ * one scale byte b per 32 consecutive columns, standing for 2^(b - 127): the row's
+ * values are code * 2^(b - 127), each exactly a bf16 number.  kalm_cache_write
+ * takes the least b in [7, 247] with max|v| <= 448 * 2^(b - 127) over the group's
+ * finite values and rounds v * 2^(127 - b) to the nearest code, ties to even (to
+ * at most 240 where b = 247): an error of at most 2^-4 of the value, or 2^-10 of
+ * the scale for values below 2^-6 of the scale.  NaN and infinities become NaN.
+ * Other bytes that a caller writes itself stand for the same numbers for
+ * 1 <= b <= 254, as far as those are bf16 numbers.
+ *
+ * Pages.  The cache has n_pages pages of page_rows rows (a power of two in
+ * [8, 1024]); page_table is int32 [n_docs][ld_table], and row i of document d is
+ * row page_table[d][i / page_rows] * page_rows + i % page_rows of codes and
+ * scales.  Documents may share pages where they are read.  codes: uint8
+ * [n_pages * page_rows][ld_codes], 16-byte aligned, ld_codes a multiple of 16;
+ * scales: uint8 [n_pages * page_rows][ld_scales].  A row whose place in the table
+ * is missing or names no page in [0, n_pages) is skipped (it reads as zeros in the
+ * attention) and flagged in the device error word.
+ * ------------------------------------------------------------------------- */
+#define KALM_CACHE_GROUP 32
+#define KALM_CACHE_MIN_PAGE_ROWS 8
+#define KALM_CACHE_MAX_PAGE_ROWS 1024
+
+/* Quantise packed rows into pages.
+ * src      [total_rows][ld_src] bf16; document d's rows are row_off[d] ..
+ *          row_off[d+1] - 1; rows that belong to no document are not read
+ * row_off  int64[n_docs + 1], ascending
+ * first_row int32[n_docs] or NULL (zeros): src row row_off[d] + i becomes row
+ *          first_row[d] + i of document d (rows appended to a cached document,
+ *          down to a single one)
+ * width    columns, a multiple of 32; a window of wider cached rows is given by
+ *          codes + column and scales + column / 32
+ * No two src rows may have the same place: which one's codes it then holds is
+ * unspecified (nothing detects that; DocumentCache in the Python package hands
+ * out distinct places).  One launch, no workspace. */
+kalm_status kalm_cache_write(const kalm_bf16* src, int64_t ld_src, const int64_t* row_off, int32_t n_docs,
+                             int64_t total_rows, int32_t width, const int32_t* first_row, const int32_t* page_table,
+                             int64_t ld_table, int32_t page_rows, int64_t n_pages, uint8_t* codes, int64_t ld_codes,
+                             uint8_t* scales, int64_t ld_scales, kalm_stream_t stream);
+
+/* Read rows back: dst[row_off[d] + i] = row first_row[d] + i of document d, the
+ * exact stored values.  Arguments as kalm_cache_write; dst [total_rows][ld_dst]
+ * bf16.  Rows that belong to no document, or are flagged, keep their contents.  A
+ * document may be named more than once.  One launch, no workspace. */
+kalm_status kalm_cache_read(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales, int64_t ld_scales,
+                            const int64_t* row_off, int32_t n_docs, int64_t total_rows, int32_t width,
+                            const int32_t* first_row, const int32_t* page_table, int64_t ld_table, int32_t page_rows,
+                            int64_t n_pages, kalm_bf16* dst, int64_t ld_dst, kalm_stream_t stream);
+
+/* kalm_merged_attention with the cross K/V read from an 8-bit cache: the same
+ * softmax over [causal self rows ; cross rows 0..Nc[d]-1], where document d's
+ * cross rows are the rows of its pages.  The keys and values are the stored
+ * numbers exactly (they are bf16 numbers, widened on the way to the tensor
+ * cores), so the result is that of kalm_merged_attention over the rows that
+ * kalm_cache_read returns.  Same passages as kalm_merged_attention.
+ *
+ * q .. total_in, max_q, total_q, n_q .. lse   as kalm_merged_attention (order from
+ *          kalm_attention_schedule for the same offsets and sizes, or NULL)
+ * k_codes, v_codes  the cached K and V columns of this layer: head g of a row at
+ *          byte g * 256; 16-byte aligned, common stride ld_codes
+ * k_scales, v_scales their scale bytes: head g at byte g * 8, common stride
+ *          ld_scales
+ * pool_off int64[n_docs + 1]: document d attends to its first Nc[d] = pool_off[d+1]
+ *          - pool_off[d] cached rows
+ * What belongs to other documents or lies behind a document's last row (self rows
+ * or cached ones) has no influence, NaN and infinities included.  Within a
+ * document, a NaN or infinity in a self V row reaches every decoder row of the
+ * query tile (128 / (n_q / n_kv) positions) that holds a row which sees it. */
+kalm_status kalm_merged_attention_cache(const kalm_bf16* q, int64_t ldq, const kalm_bf16* k_self,
+                                        const kalm_bf16* v_self, int64_t ld_self, const uint8_t* k_codes,
+                                        const uint8_t* v_codes, int64_t ld_codes, const uint8_t* k_scales,
+                                        const uint8_t* v_scales, int64_t ld_scales, const int32_t* page_table,
+                                        int64_t ld_table, int32_t page_rows, int64_t n_pages, const int64_t* q_off,
+                                        const int64_t* in_off, int64_t total_in, const int64_t* pool_off,
+                                        int32_t n_docs, int32_t max_q, int64_t total_q, int32_t n_q, int32_t n_kv,
+                                        int32_t head_dim, float scale, int32_t last_tile_only, const int32_t* order,
+                                        kalm_bf16* out, int64_t ldo, float* lse, kalm_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The norms around a decoder block.
+ * "KaLM-Reranker-V1-Nano - MLX (Apple Silicon)", "Derivation": the decoder's layers
+ * are those of the base model's configuration; reading taken (the pages do not
+ * spell them out): RMS norms, norm(v, w) = v / sqrt(mean(v^2) + eps) *
+ * (w + weight_offset), with weight_offset 1 where a checkpoint stores w - 1.
+ * fp32 from the loads to one rounding to bf16 per output.
+ * ------------------------------------------------------------------------- */
+#define KALM_NORM_MAX_WIDTH 16384
+
+/* h = norm(x, w): the norm before a block.
+ * x [rows][ldx], w [width], h [rows][ldh] bf16; h may be x (same stride).
+ * width a multiple of 8 up to KALM_NORM_MAX_WIDTH; eps > 0. */
+kalm_status kalm_rms_norm(const kalm_bf16* x, int64_t ldx, const kalm_bf16* w, kalm_bf16* h, int64_t ldh,
+                          int64_t rows, int32_t width, float eps, float weight_offset, kalm_stream_t stream);
+
+/* Between two blocks, in one pass:
+ *   t = residual_scale * x + gate * norm(y, w_post);  x_out = t;  h = norm(t, w_pre)
+ * h is the norm of t before its rounding.
+ * y        [rows][ldy] the first block's output
+ * x        [rows][ldx] the residual stream
+ * w_post   [width] or NULL: y enters without a norm
+ * gate     NULL: 1; with ld_gate = 0 one vector [width] for all rows; else
+ *          [n_docs][ld_gate], document d's gate for rows q_off[d] .. q_off[d+1] - 1
+ * q_off    int64[n_docs + 1] or NULL: with it, only the documents' rows are computed
+ *          and the outputs' other rows keep their contents
+ * x_out    [rows][ldxo]; may be x or y (same stride)
+ * w_pre, h [width] and [rows][ldh], or both NULL; h may be y (same stride, where
+ *          x_out is not) */
+kalm_status kalm_norm_residual(const kalm_bf16* y, int64_t ldy, const kalm_bf16* x, int64_t ldx,
+                               const kalm_bf16* w_post, const kalm_bf16* gate, int64_t ld_gate, const int64_t* q_off,
+                               int32_t n_docs, float residual_scale, kalm_bf16* x_out, int64_t ldxo,
+                               const kalm_bf16* w_pre, kalm_bf16* h, int64_t ldh, int64_t rows, int32_t width,
+                               float eps, float weight_offset, kalm_stream_t stream);
 
 /* Failure-detection self-test: one CTA waits on a shared-memory barrier that
  * nothing completes, with a bound of `wait_ns` nanoseconds; on expiry it

@@ -1,0 +1,354 @@
+"""The 8-bit document cache on the GPU: quantising rows as they are written, reading them back, and the merged
+attention over cached rows, against plain 64-bit implementations.
+
+Tolerances.  Codes, scales and read-back values are exact.  The attention: the stored keys and values are the
+operands, so what is off is (a) the output's rounding to bf16, at most 2^-8 of it (half a step), (b) each
+probability's rounding to bf16, 2^-8 of it, so at most 2^-8 * sum_j p_j |v_j| <= 2^-8 max|v|, and (c) fp32
+effects: logits up to 40 in magnitude with 2^-22 relative error and ex2 with 2^-22, below 2^-16 max|v|.
+A bound of 2^-8 |o| + 2^-8 max|v| + 2^-15 max|v| per element holds for all.  The log-sum-exp: 256-term fp32 sums of
+exact products, error below 2^-24 * 256 * sum|q k| / 16 < 1e-4 for the inputs here, plus ex2 / log2 effects of 2^-20.
+"""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import oracle
+from tests.gpu_util import f64_to_dev, from_dev, i32, i64, rand_bf16
+
+pytestmark = pytest.mark.gpu
+
+GROUP = 32
+
+
+@pytest.fixture(scope="module")
+def kalm():
+    import __graft_entry__
+    __graft_entry__.build()
+    import encoder_decoder_document_b200 as k
+    k.kalm_device_check()
+    return k
+
+
+# ------------------------------------------------------------------ plain forms, 64 bits
+def e4m3_value(codes):
+    c = codes.astype(np.int64)
+    exp, frac = (c >> 3) & 15, c & 7
+    mag = np.where(exp == 0, frac * 2.0 ** -9, (1 + frac / 8) * 2.0 ** (exp - 7.0))
+    mag = np.where((c & 127) == 127, np.nan, mag)
+    return np.where(c >= 128, -mag, mag)
+
+
+ALL = e4m3_value(np.arange(127))  # the non-negative codes' values, ascending
+
+
+def nearest_code(t):
+    """Nearest e4m3 number of |t| <= 448, ties to the even code."""
+    hi = np.clip(np.searchsorted(ALL, t), 1, 126)
+    lo = hi - 1
+    dl, dh = t - ALL[lo], ALL[hi] - t
+    return np.where(dl < dh, lo, np.where(dh < dl, hi, np.where(lo % 2 == 0, lo, hi)))
+
+
+def quantise(v):
+    """Codes and scale bytes of [rows][width] bf16-valued float64 rows, from the definition."""
+    g = v.reshape(v.shape[0], -1, GROUP)
+    fine = np.isfinite(g)
+    top = np.where(fine, np.abs(g), 0.0).max(-1)
+    e = np.full(top.shape, -120)
+    while (top > 448.0 * 2.0 ** e).any():
+        e = e + (top > 448.0 * 2.0 ** e)
+    t = np.abs(np.where(fine, g, 0.0)) / 2.0 ** e[..., None]
+    t = np.where((e >= 120)[..., None], np.minimum(t, 240.0), t)
+    code = nearest_code(t)
+    code = np.where(fine, code, 127)
+    # the sign bit of a NaN's code is not specified
+    code = np.where(np.signbit(g) & fine, code + 128, code)
+    return code.reshape(v.shape).astype(np.uint8), (e + 127).astype(np.uint8)
+
+
+def dequantise(codes, scales):
+    return e4m3_value(codes) * np.repeat(2.0 ** (scales.astype(np.float64) - 127), GROUP, -1)
+
+
+def make_pages(rng, rows, page_rows, spare=2):
+    need = [-(-int(r) // page_rows) for r in rows]
+    n_pages = sum(need) + spare
+    perm = rng.permutation(n_pages)
+    table = np.full((len(rows), max(max(need, default=0), 1)), -1, np.int32)
+    k = 0
+    for d, n in enumerate(need):
+        table[d, :n] = perm[k:k + n]
+        k += n
+    return table, n_pages
+
+
+def row_index(table, page_rows, d, first, n):
+    i = np.arange(first, first + n)
+    return table[d, i // page_rows].astype(np.int64) * page_rows + i % page_rows
+
+
+def offsets(n):
+    return np.concatenate([[0], np.cumsum(n)]).astype(np.int64)
+
+
+def same_codes(got, want):
+    """Equal codes, any NaN for a NaN, and either zero for a zero that was rounded to."""
+    nan = (want & 127) == 127
+    assert (((got & 127) == 127) == nan).all()
+    np.testing.assert_array_equal(got[~nan], want[~nan])
+
+
+# ------------------------------------------------------------------ write
+@pytest.mark.parametrize("rows,first,width,page_rows", [
+    ([1], [0], 32, 8),                       # one row, one group
+    ([1, 1, 1], [40, 7, 63], 640, 64),       # single rows appended, at a page's end too
+    ([0, 5, 0, 0, 17, 1], None, 96, 8),      # empty documents, odd counts
+    ([256, 33, 64, 129], None, 640, 64),
+    ([70, 3], [5, 250], 9216, 16),           # every layer's cross K/V of a wide stack
+    ([1] * 300, None, 32, 8),                # a warp's rows span many documents
+    ([1000], [24], 64, 1024),
+])
+def test_write(kalm, rows, first, width, page_rows):
+    rng = np.random.default_rng(sum(rows) + width)
+    n0 = np.zeros(len(rows), int) if first is None else np.asarray(first)
+    table, n_pages = make_pages(rng, np.asarray(rows) + n0, page_rows)
+    off = offsets(rows)
+    total = int(off[-1])
+    v = rand_bf16(rng, (total, width)) * 2.0 ** rng.integers(-6, 7, (total, 1))
+    v[:, ::7] *= 2.0 ** -9   # below the group's normal range
+    src = torch.full((total + 3, width + 8), float("nan"), dtype=torch.bfloat16, device="cuda")
+    src[:total, :width] = f64_to_dev(v)
+    codes = torch.full((n_pages * page_rows, width + 16), 0x55, dtype=torch.uint8, device="cuda")
+    scales = torch.full((n_pages * page_rows, width // 32 + 3), 0x11, dtype=torch.uint8, device="cuda")
+    want_c, want_s = codes.cpu().numpy(), scales.cpu().numpy()
+    c, s = quantise(v)
+    for d in range(len(rows)):
+        at = row_index(table, page_rows, d, n0[d], rows[d])
+        want_c[at, :width], want_s[at, :width // 32] = c[off[d]:off[d + 1]], s[off[d]:off[d + 1]]
+    # three rows behind the last document, and strides wider than the rows: left as they were
+    kalm.kalm_cache_write(src[:, :width], i64(off), i32(table), page_rows, codes[:, :width], scales[:, :width // 32],
+                          first_row=None if first is None else i32(first))
+    assert kalm.kalm_check_device_errors() == 0
+    np.testing.assert_array_equal(codes.cpu().numpy(), want_c)
+    np.testing.assert_array_equal(scales.cpu().numpy(), want_s)
+
+
+def test_write_special_values(kalm):
+    """Zeros, subnormals, the borders of a scale, ties, the largest values, NaN and infinities."""
+    big = float(torch.finfo(torch.bfloat16).max)
+    rows = [[0.0] * 32, [-0.0] * 32, [2.0 ** -133] * 32, [448.0, 447.0] * 16, [450.0, 1.0] * 16, [1.75, 1.7578125] * 16,
+            [big, -big] * 16, [big, 1.0] * 16, [2.0 ** 127, 3.0] * 16, [float("nan"), 1.0] * 16,
+            [float("inf"), -2.0] * 16, [float("-inf")] * 32, [448.0] + [(k + 0.5) * 2.0 ** -9 for k in range(31)],
+            [448.0] + [17.0, 19.0, 21.0, 23.0] * 7 + [0.0, -0.0, 2.0 ** -10]]
+    v = oracle.bf16_round(np.array(rows)) if np.isfinite(np.array(rows)).all() else np.array(rows)
+    t = torch.tensor(rows, dtype=torch.float64).to(torch.bfloat16)
+    v = t.double().numpy()
+    want_c, want_s = quantise(v)
+    n = len(rows)
+    codes = torch.zeros(16, 32, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(16, 1, dtype=torch.uint8, device="cuda")
+    kalm.kalm_cache_write(t.cuda(), i64([0, n]), i32([[1, 0]]), 8, codes, scales)
+    at = row_index(np.array([[1, 0]]), 8, 0, 0, n)
+    got_c, got_s = codes.cpu().numpy()[at], scales.cpu().numpy()[at]
+    same_codes(got_c, want_c)
+    np.testing.assert_array_equal(got_s, want_s)
+    assert want_s.min() >= 7 and want_s.max() <= 247
+    # what is read back is the exact number, finite wherever the source was
+    dst = torch.empty(n, 32, dtype=torch.bfloat16, device="cuda")
+    kalm.kalm_cache_read(codes, scales, i64([0, n]), i32([[1, 0]]), 8, dst)
+    back = dst.double().cpu().numpy()
+    np.testing.assert_array_equal(np.isfinite(back), np.isfinite(v))
+    np.testing.assert_array_equal(back[np.isfinite(v)], dequantise(want_c, want_s)[np.isfinite(v)])
+    assert kalm.kalm_check_device_errors() == 0
+
+
+def test_every_code_and_scale_reads_back_exactly(kalm):
+    """All 256 codes under the scales that kalm_cache_write writes."""
+    bytes_ = np.arange(7, 248)
+    codes = np.tile(np.arange(256, dtype=np.uint8), (len(bytes_), 1))
+    scales = np.repeat(bytes_.astype(np.uint8)[:, None], 8, 1)
+    want = dequantise(codes, scales)
+    n = len(bytes_)
+    pad = -(-n // 8) * 8
+    c = torch.zeros(pad, 256, dtype=torch.uint8, device="cuda")
+    s = torch.zeros(pad, 8, dtype=torch.uint8, device="cuda")
+    c[:n], s[:n] = torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda()
+    dst = torch.empty(n, 256, dtype=torch.bfloat16, device="cuda")
+    kalm.kalm_cache_read(c, s, i64([0, n]), i32(np.arange(pad // 8)[None]), 8, dst)
+    got = dst.double().cpu().numpy()
+    held = np.abs(want) < 2.0 ** 128  # kalm_cache_write never stores more than 240 under its largest scale
+    np.testing.assert_array_equal(got[held & ~np.isnan(want)], want[held & ~np.isnan(want)])
+    assert np.isnan(got[np.isnan(want)]).all()
+
+
+# ------------------------------------------------------------------ read
+@pytest.mark.parametrize("rows,first,width,page_rows", [
+    ([1], [9], 32, 8),
+    ([0, 5, 0, 17], None, 640, 16),
+    ([100, 1, 64, 65], [3, 0, 64, 1], 2560, 64),
+    ([1] * 200, None, 64, 8),
+])
+def test_read(kalm, rows, first, width, page_rows):
+    rng = np.random.default_rng(sum(rows) + width + 1)
+    n0 = np.zeros(len(rows), int) if first is None else np.asarray(first)
+    table, n_pages = make_pages(rng, np.asarray(rows) + n0, page_rows)
+    codes, scales = quantise(rand_bf16(rng, (n_pages * page_rows, width)))
+    full_c = torch.zeros(n_pages * page_rows, width + 32, dtype=torch.uint8, device="cuda")
+    full_s = torch.zeros(n_pages * page_rows, width // 32 + 1, dtype=torch.uint8, device="cuda")
+    full_c[:, 32:], full_s[:, 1:] = torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda()  # a column window
+    off = offsets(rows)
+    total = int(off[-1])
+    dst = torch.full((total + 2, width + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    kalm.kalm_cache_read(full_c[:, 32:], full_s[:, 1:], i64(off), i32(table), page_rows, dst[:, :width],
+                         first_row=None if first is None else i32(first))
+    assert kalm.kalm_check_device_errors() == 0
+    want = np.full((total + 2, width + 8), 7.0)
+    for d in range(len(rows)):
+        at = row_index(table, page_rows, d, n0[d], rows[d])
+        want[off[d]:off[d + 1], :width] = dequantise(codes[at], scales[at])
+    np.testing.assert_array_equal(from_dev(dst), want)
+
+
+def test_read_names_a_document_twice(kalm):
+    rng = np.random.default_rng(3)
+    codes, scales = quantise(rand_bf16(rng, (32, 64)))
+    c, s = torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda()
+    dst = torch.empty(40, 64, dtype=torch.bfloat16, device="cuda")
+    kalm.kalm_cache_read(c, s, i64([0, 20, 40]), i32([[3, 0, 2], [3, 0, 2]]), 8, dst)
+    got = from_dev(dst)
+    np.testing.assert_array_equal(got[:20], got[20:])
+    assert kalm.kalm_check_device_errors() == 0
+
+
+def test_bad_pages_are_flagged_and_skipped(kalm):
+    """Page numbers outside the cache and rows past the table: nothing is written or read there."""
+    src = torch.ones(30, 32, dtype=torch.bfloat16, device="cuda")
+    codes = torch.full((16, 32), 3, dtype=torch.uint8, device="cuda")
+    scales = torch.full((16, 1), 5, dtype=torch.uint8, device="cuda")
+    # document 0: page 1, then a page that does not exist, then -1; the last rows lie past the table
+    table = i32([[1, 2, -1]])
+    kalm.kalm_cache_write(src, i64([0, 30]), table, 8, codes, scales)
+    with pytest.raises(kalm.KalmError) as e:
+        kalm.kalm_check_device_errors()
+    assert e.value.name == "KALM_ERR_DEVICE_ARG"
+    got = codes.cpu().numpy()
+    assert (got[:8] == 3).all() and (got[8:] == quantise(np.ones((8, 32)))[0]).all()
+    dst = torch.full((30, 32), 9.0, dtype=torch.bfloat16, device="cuda")
+    kalm.kalm_cache_read(codes, scales, i64([0, 30]), table, 8, dst)
+    with pytest.raises(kalm.KalmError):
+        kalm.kalm_check_device_errors()
+    back = from_dev(dst)
+    assert (back[:8] == 1.0).all() and (back[8:] == 9.0).all()
+    # a first row before the document's start
+    kalm.kalm_cache_write(src[:4], i64([0, 4]), table, 8, codes, scales, first_row=i32([-2]))
+    with pytest.raises(kalm.KalmError):
+        kalm.kalm_check_device_errors()
+
+
+# ------------------------------------------------------------------ attention over the cache
+def attention(rng, lq, nc, n_q, n_kv, page_rows, q_std=0.7, c_std=0.7, window=0, spare=2):
+    """Inputs: decoder rows, and a cache whose columns hold `window` other columns before this layer's K and V."""
+    d = 256
+    q_off, p_off = offsets(lq), offsets(nc)
+    table, n_pages = make_pages(rng, nc, page_rows, spare)
+    n = n_pages * page_rows
+    cache = rand_bf16(rng, (n, 2 * n_kv * d), c_std)
+    codes, scales = quantise(cache)
+    r = int(q_off[-1])
+    a = dict(lq=lq, nc=nc, n_q=n_q, n_kv=n_kv, page_rows=page_rows, q_off=q_off, p_off=p_off, table=table,
+             q=rand_bf16(rng, (r, n_q, d), q_std), ks=rand_bf16(rng, (r, n_kv, d), q_std), vs=rand_bf16(rng, (r, n_kv, d)),
+             codes=codes, scales=scales, window=window)
+    return a
+
+
+def cached_rows(a, d):
+    return row_index(a["table"], a["page_rows"], d, 0, a["nc"][d])
+
+
+def plain_attention(a, scale=1 / 16, in_off=None):
+    """64-bit: out [rows][n_q][256], lse [rows][n_q], and a bound's ingredients (max |v| of each row's document)."""
+    n_q, n_kv, d = a["n_q"], a["n_kv"], 256
+    r = int(a["q_off"][-1])
+    out, lse, vmax = np.zeros((r, n_q, d)), np.zeros((r, n_q)), np.zeros((r, n_q))
+    val = dequantise(a["codes"], a["scales"])
+    for i in range(len(a["lq"])):
+        r0, r1 = a["q_off"][i], a["q_off"][i + 1]
+        s0 = r0 if in_off is None else in_off[i]
+        n = r1 - r0
+        c = val[cached_rows(a, i)].reshape(-1, 2, n_kv, d)
+        for h in range(n_q):
+            g = h // (n_q // n_kv)
+            q, k, v = a["q"][s0:s0 + n, h], a["ks"][s0:s0 + n, g], a["vs"][s0:s0 + n, g]
+            ls = np.where(np.tri(n, dtype=bool), q @ k.T * scale, -np.inf)
+            logits = np.concatenate([ls, q @ c[:, 0, g].T * scale], 1)
+            m = logits.max(1, keepdims=True)
+            p = np.exp(logits - m)
+            z = p.sum(1, keepdims=True)
+            vv = np.concatenate([v, c[:, 1, g]])
+            out[r0:r1, h] = p / z @ vv
+            lse[r0:r1, h] = (m + np.log(z))[:, 0]
+            vmax[r0:r1, h] = np.abs(vv).max() if vv.size else 0
+    return out, lse, vmax
+
+
+def run_attention(kalm, a, scale=1 / 16, order=None, in_off=None, last=False, poison=False, stream=None, page_table=None):
+    d, n_q, n_kv = 256, a["n_q"], a["n_kv"]
+    rows = a["q"].shape[0]
+    q_off, p_off = i64(a["q_off"]), i64(a["p_off"])
+    r = int(a["q_off"][-1])
+    qkv = torch.cat([f64_to_dev(a[k].reshape(rows, -1)) for k in ("q", "ks", "vs")], 1)
+    w, win = n_kv * d, a["window"]
+    n = a["codes"].shape[0]
+    codes = torch.full((n, win + 2 * w), 0x7F, dtype=torch.uint8, device="cuda")
+    scales = torch.full((n, (win + 2 * w) // 32), 0x7F, dtype=torch.uint8, device="cuda")
+    codes[:, win:] = torch.from_numpy(a["codes"]).cuda()
+    scales[:, win // 32:] = torch.from_numpy(a["scales"]).cuda()
+    if poison:  # every cached row that belongs to no document's attended rows holds NaN
+        used = np.zeros(n, bool)
+        for i in range(len(a["nc"])):
+            used[cached_rows(a, i)] = True
+        codes[torch.from_numpy(~used).cuda()] = 0x7F
+    out = torch.full((r, n_q * d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((r, n_q), float("nan"), dtype=torch.float32, device="cuda")
+    kc, vc = codes[:, win:win + w], codes[:, win + w:]
+    ksc, vsc = scales[:, win // 32:(win + w) // 32], scales[:, (win + w) // 32:]
+    kalm.kalm_merged_attention_cache(
+        qkv[:, :n_q * d], qkv[:, n_q * d:n_q * d + w], qkv[:, n_q * d + w:], kc, ksc, vc, vsc,
+        i32(a["table"]) if page_table is None else page_table, a["page_rows"], q_off, p_off, max(a["lq"]), n_q, n_kv, out,
+        scale, lse, in_off=None if in_off is None else i64(in_off), last_tile_only=last,
+        order=order(q_off, p_off) if order else None, stream=stream)
+    if stream is not None:
+        stream.synchronize()
+    return from_dev(out).reshape(r, n_q, d), lse.cpu().numpy().astype(np.float64)
+
+
+def check(got, lse, want, want_lse, vmax):
+    bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + 2.0 ** -15) * vmax[..., None]
+    over = np.abs(got - want) / bound
+    assert np.isfinite(got).all()
+    assert over.max() <= 1.0, over.max()
+    assert np.abs(lse - want_lse).max() <= 1e-4 + 2.0 ** -20 * np.abs(want_lse).max()
+
+
+SHAPES = [
+    ([1], [1], 1, 1, 8),                                   # one position, one cached row, one head
+    ([1, 1, 1], [0, 64, 200], 4, 1, 64),                   # single tokens
+    ([32, 32, 32, 32], [3, 16, 9, 1], 4, 1, 16),           # Tiny shape
+    ([128] * 6, [256, 16, 1, 0, 255, 64], 4, 1, 64),       # Nano shape, an empty document, ragged tails
+    ([1, 2, 31, 33, 65, 130], [0, 5, 64, 65, 128, 129], 4, 1, 32),
+    ([256, 100], [75, 256], 8, 4, 8),                      # Large heads, pages that end inside a tile
+    ([512, 3], [1024, 2], 4, 1, 1024),                     # query budget, chunk 1
+    ([17, 64, 200], [7, 0, 100], 2, 2, 16),                # one query head per KV head
+    ([40, 130], [20, 70], 8, 1, 128),                      # 8 query heads per KV head
+    ([5, 9], [0, 0], 4, 1, 8),                             # nothing cached in the whole batch
+    ([3] * 200, list(range(0, 200)), 4, 1, 16),            # more items than CTAs
+]
+
+
+@pytest.mark.parametrize("lq,nc,n_q,n_kv,page_rows", SHAPES)
+def test_attention(kalm, lq, nc, n_q, n_kv, page_rows):
+    a = attention(np.random.default_rng(sum(lq) + sum(nc) + n_q), lq, nc, n_q, n_kv, page_rows, window=0 if n_kv > 1 else 512)
+    got, lse = run_attention(kalm, a, poison=True)
+    assert kalm.kalm_check_device_errors() == 0
+    check(got, lse, *plain_attention(a))
