@@ -22,7 +22,8 @@ __all__ = [
     "kalm_merged_attention_out_proj", "kalm_merged_attention_out_proj_static", "kalm_attention_out_proj_sync_len",
     "kalm_yes_no_score", "kalm_broadcast_rows", "kalm_selftest_wait_timeout", "kalm_attention_items",
     "kalm_attention_schedule", "kalm_rope", "kalm_rope_table", "kalm_linear_rope",
-    "kalm_cache_write", "kalm_cache_read", "kalm_merged_attention_cache", "kalm_rms_norm", "kalm_norm_residual",
+    "kalm_cache_write", "kalm_cache_read", "kalm_merged_attention_cache",
+    "kalm_merged_attention_cache_rows", "kalm_rms_norm", "kalm_norm_residual",
 ]
 
 HEAD_DIM = 256
@@ -362,11 +363,14 @@ def kalm_merged_attention_cache(q: torch.Tensor, k_self: torch.Tensor, v_self: t
                                 lse: Optional[torch.Tensor] = None, head_dim: int = HEAD_DIM,
                                 in_off: Optional[torch.Tensor] = None, last_tile_only: bool = False,
                                 total_q: Optional[int] = None, order: Optional[torch.Tensor] = None,
-                                stream=None) -> None:
+                                workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """kalm_merged_attention with the cross K/V of an 8-bit document cache: document d attends to its
     first pool_off[d+1] - pool_off[d] cached rows.  k/v codes uint8 [cache rows][n_kv * head_dim]
     (column views of the cached rows are fine), k/v scales uint8 [cache rows][n_kv * head_dim / 32];
-    the other arguments as kalm_merged_attention."""
+    the other arguments as kalm_merged_attention.
+
+    workspace: bf16 scratch [>= kalm_merged_attention_cache_rows(cached rows, n_docs)][2 * n_kv * head_dim];
+    None allocates one for this call, for as many rows as the page table has places."""
     where = "kalm_merged_attention_cache"
     if scale is None:
         scale = head_dim ** -0.5
@@ -395,12 +399,25 @@ def kalm_merged_attention_cache(q: torch.Tensor, k_self: torch.Tensor, v_self: t
         raise KalmError(1, where, f"lse: expected a contiguous [{total_q}][{n_q}] tensor")
     if order is not None and order.numel() < kalm_attention_items(n_docs, max_q, n_q, n_kv, last_tile_only):
         raise KalmError(1, where, "order is shorter than the call's work items")
+    if workspace is None:
+        with torch.cuda.stream(stream):  # the allocator hands memory out per stream
+            workspace = torch.empty(n_docs * (ld_table * page_rows + 64), 2 * n_kv * head_dim, dtype=torch.bfloat16,
+                                    device=q.device)
+    else:
+        _check(where, torch.bfloat16, workspace)
+        if workspace.dim() != 2 or not workspace.is_contiguous() or workspace.shape[1] != 2 * n_kv * head_dim:
+            raise KalmError(1, where, f"workspace: expected a contiguous [rows][{2 * n_kv * head_dim}] tensor")
     call(where, q.data_ptr(), ldq, k_self.data_ptr(), v_self.data_ptr(), ld_self, k_codes.data_ptr(),
          v_codes.data_ptr(), ld_codes, k_scales.data_ptr(), v_scales.data_ptr(), ld_scales, page_table.data_ptr(),
          ld_table, page_rows, n_pages, q_off.data_ptr(), None if in_off is None else in_off.data_ptr(), rows,
          pool_off.data_ptr(), n_docs, int(max_q), int(total_q), n_q, n_kv, head_dim, float(scale),
-         1 if last_tile_only else 0, None if order is None else order.data_ptr(), out.data_ptr(), ldo,
-         None if lse is None else lse.data_ptr(), _stream(stream))
+         1 if last_tile_only else 0, None if order is None else order.data_ptr(), workspace.data_ptr(),
+         workspace.shape[0], out.data_ptr(), ldo, None if lse is None else lse.data_ptr(), _stream(stream))
+
+
+def kalm_merged_attention_cache_rows(total_pool: int, n_docs: int) -> int:
+    """Rows of kalm_merged_attention_cache's workspace (-1 for negative sizes)."""
+    return int(load().kalm_merged_attention_cache_rows(total_pool, n_docs))
 
 
 def kalm_rms_norm(x: torch.Tensor, w: torch.Tensor, h: torch.Tensor, eps: float = 1e-6, weight_offset: float = 0.0,

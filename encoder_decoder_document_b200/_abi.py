@@ -60,12 +60,13 @@ SIGNATURES = {
                         c_i64, c_vp],
     "kalm_merged_attention_cache": [c_vp, c_i64, c_vp, c_vp, c_i64, c_vp, c_vp, c_i64, c_vp, c_vp, c_i64, c_vp, c_i64,
                                     c_i32, c_i64, c_vp, c_vp, c_i64, c_vp, c_i32, c_i32, c_i64, c_i32, c_i32, c_i32,
-                                    c_f32, c_i32, c_vp, c_vp, c_i64, c_vp, c_vp],
+                                    c_f32, c_i32, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp],
+    "kalm_merged_attention_cache_rows": [c_i64, c_i32],
     "kalm_rms_norm": [c_vp, c_i64, c_vp, c_vp, c_i64, c_i64, c_i32, c_f32, c_f32, c_vp],
     "kalm_norm_residual": [c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_i64, c_vp, c_i32, c_f32, c_vp, c_i64, c_vp, c_vp,
                            c_i64, c_i64, c_i32, c_f32, c_f32, c_vp],
 }
-_RESTYPE = {"kalm_version": c_i32, "kalm_attention_items": c_i64, "kalm_attention_out_proj_sync_len": c_i64, "kalm_linear_chain_sync_len": c_i64, "kalm_status_string": ctypes.c_char_p, "kalm_last_error": ctypes.c_char_p}
+_RESTYPE = {"kalm_version": c_i32, "kalm_attention_items": c_i64, "kalm_attention_out_proj_sync_len": c_i64, "kalm_linear_chain_sync_len": c_i64, "kalm_merged_attention_cache_rows": c_i64, "kalm_status_string": ctypes.c_char_p, "kalm_last_error": ctypes.c_char_p}
 
 
 class KalmError(RuntimeError):

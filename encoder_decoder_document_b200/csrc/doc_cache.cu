@@ -9,10 +9,11 @@
 // The product with 2^-e is exact, so a value is rounded once, by at most 2^-4 of itself (half a step of a
 // 3-bit mantissa; 2^-10 * 2^e where it is below the normal range).
 //
-// Both kernels stream: bound by HBM, 3 + 1/32 bytes a value.  A lane takes 8 columns (16 bytes of bf16, 8 bytes
-// of codes), so a warp's loads and stores are runs of whole lines on both sides and four neighbouring lanes
-// hold one scale group; kUnits such slices per lane are loaded before the first is used.  A warp's units are
-// consecutive, so it searches the document of its first row once (32 offsets a round) and walks on from there.
+// Both kernels stream: bound by HBM, 3 + 1/32 bytes a value.  A lane takes 16 columns (32 bytes of bf16 in
+// one access where the rows allow it, 16 bytes of codes), so a warp's loads and stores are runs of whole lines
+// on both sides and two neighbouring lanes hold one scale group; kUnits such slices per lane are loaded before the
+// first is used.  A warp's units are consecutive, so it searches the document of its first row once (128 offsets a
+// round) and walks on from there.
 #include "kalm.h"
 #include "kalm_cache.cuh"
 #include "kalm_internal.h"
@@ -22,16 +23,20 @@ namespace kalm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnits = 4;  // 8-column slices a lane keeps in flight
+constexpr int kUnits = 4;    // 16-column slices a lane keeps in flight
+constexpr int kUnitCols = 16;
 
 // The document that holds packed row r: the largest d with off[d] <= r (0 if none).  A warp searches together.
 __device__ __forceinline__ int find_doc_warp(const int64_t* __restrict__ off, int n_docs, int64_t r, int lane) {
   int lo = 0, hi = n_docs;  // off[lo] <= r < off[hi], taking off[0] <= r
   while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32;
-    const int at = lo + step * (lane + 1);
-    const unsigned below = __ballot_sync(0xffffffffu, at < hi && __ldg(off + at) <= r);
-    const int n = __popc(below);
+    const int step = (hi - lo + 127) / 128;
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int at = lo + step * (32 * j + lane + 1);
+      n += __popc(__ballot_sync(0xffffffffu, at < hi && __ldg(off + at) <= r));
+    }
     hi = min(hi, lo + step * (n + 1));
     lo += step * n;
   }
@@ -43,13 +48,13 @@ struct Rows {
   const int32_t* first;  // [n_docs] row of the document that its first packed row becomes, or NULL: 0
   int n_docs;
   int64_t total;         // packed rows in memory; those from off[n_docs] on belong to no document
-  int upr;               // 8-column units of a row
+  int upr;               // units of a row
 };
 
 // A lane's units: their packed rows and columns, and the cache rows they belong to (-1: none).
 struct Unit {
   int64_t row, at;
-  int col;
+  int col;  // in units
 };
 
 __device__ __forceinline__ void locate(Unit (&u)[kUnits], const Rows& rows, const CachePages& pages, uint32_t* err) {
@@ -100,6 +105,29 @@ __device__ __forceinline__ int group_exp(uint32_t top) {
   return max(e, kCacheMinExp);
 }
 
+// 16 values of a row; WIDE: the rows are 32-byte aligned.
+template <bool WIDE>
+__device__ __forceinline__ Words8 load16(const uint4* p) {
+  if (WIDE) return ldg_words8(p);
+  const uint4 a = __ldg(p), b = __ldg(p + 1);
+  return Words8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+}
+template <bool WIDE>
+__device__ __forceinline__ void store16(uint4* p, const Words8& v) {
+  if (WIDE) {
+    stg_words8(p, v);
+  } else {
+    p[0] = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+    p[1] = make_uint4(v.w[4], v.w[5], v.w[6], v.w[7]);
+  }
+}
+
+__device__ __forceinline__ uint32_t pair_max(uint32_t v) { return max(v, __shfl_xor_sync(0xffffffffu, v, 1)); }
+
+// Magnitude bits of value k of 16.
+__device__ __forceinline__ uint32_t magnitude(const Words8& x, int k) { return (x.w[k >> 1] >> (16 * (k & 1))) & 0x7fffu; }
+
+template <bool WIDE>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const uint4* __restrict__ src, int64_t ld_src_v,
                                                                const Rows rows, const CachePages pages,
                                                                uint8_t* __restrict__ codes, int64_t ld_codes,
@@ -109,70 +137,59 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const uint4* __re
   pdl_wait_predecessor();
   Unit u[kUnits];
   locate(u, rows, pages, err);
-  uint4 x[kUnits];
+  Words8 x[kUnits];
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
-    x[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (u[i].at >= 0) x[i] = __ldg(src + u[i].row * ld_src_v + u[i].col);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[i].w[k] = 0;
+    if (u[i].at >= 0) x[i] = load16<WIDE>(src + u[i].row * ld_src_v + u[i].col * 2);
   }
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    const Words8& v = x[i];
     // largest magnitude: bf16 magnitudes order as their bits do
     uint32_t m2 = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) m2 = __vmaxu2(m2, w[k] & 0x7fff7fffu);
-    uint32_t top = max(m2 & 0xffffu, m2 >> 16);
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    for (int k = 0; k < 8; ++k) m2 = __vmaxu2(m2, v.w[k] & 0x7fff7fffu);
+    uint32_t top = pair_max(max(m2 & 0xffffu, m2 >> 16));
     const bool odd = top >= 0x7f80u;  // an infinity or NaN in the group: the scale is the finite values'
-    if (odd) {
-      top = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t b = (w[k >> 1] >> (16 * (k & 1))) & 0x7fffu;
-        if (b < 0x7f80u) top = max(top, b);
-      }
-    }
     if (__any_sync(0xffffffffu, odd)) {
-      uint32_t o = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      o = max(o, __shfl_xor_sync(0xffffffffu, o, 2));
-      if (odd) top = o;
+      uint32_t fine = 0;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) fine = max(fine, magnitude(v, k) < 0x7f80u ? magnitude(v, k) : 0u);
+      fine = pair_max(fine);
+      if (odd) top = fine;
     }
     const int e = group_exp(top);
     const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    const float lim = e >= kCacheMaxExp ? 240.f : 448.f;
-    float v[8];
+    float f[16];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[2 * k] = __uint_as_float(w[k] << 16) * inv;
-      v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u) * inv;
+    for (int k = 0; k < 8; ++k) {
+      f[2 * k] = __uint_as_float(v.w[k] << 16) * inv;
+      f[2 * k + 1] = __uint_as_float(v.w[k] & 0xffff0000u) * inv;
     }
     if (odd || e >= kCacheMaxExp) {
+      const float lim = e >= kCacheMaxExp ? 240.f : 448.f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t b = (w[k >> 1] >> (16 * (k & 1))) & 0x7fffu;
-        // an infinity is stored as NaN: no finite code may stand for it
-        v[k] = b >= 0x7f80u ? __uint_as_float(0x7fffffffu) : fminf(fmaxf(v[k], -lim), lim);
-      }
+      for (int k = 0; k < 16; ++k)  // an infinity is stored as NaN: no finite code may stand for it
+        f[k] = magnitude(v, k) >= 0x7f80u ? __uint_as_float(0x7fffffffu) : fminf(fmaxf(f[k], -lim), lim);
     }
-    uint2 out;
-    uint32_t* o = &out.x;
+    uint32_t out[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * k], v[2 * k + 1]), __NV_SATFINITE, __NV_E4M3);
-      if (k & 1)
-        o[k >> 1] |= two << 16;
-      else
-        o[k >> 1] = two;
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * k], f[4 * k + 1]), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * k + 2], f[4 * k + 3]), __NV_SATFINITE, __NV_E4M3);
+      out[k] = lo | hi << 16;
     }
     if (u[i].at >= 0) {
-      *reinterpret_cast<uint2*>(codes + u[i].at * ld_codes + u[i].col * 8) = out;
-      if ((u[i].col & 3) == 0) scales[u[i].at * ld_scales + (u[i].col >> 2)] = static_cast<uint8_t>(e + 127);
+      *reinterpret_cast<uint4*>(codes + u[i].at * ld_codes + u[i].col * kUnitCols) =
+          make_uint4(out[0], out[1], out[2], out[3]);
+      if ((u[i].col & 1) == 0) scales[u[i].at * ld_scales + (u[i].col >> 1)] = static_cast<uint8_t>(e + 127);
     }
   }
 }
 
+template <bool WIDE>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const uint8_t* __restrict__ codes, int64_t ld_codes,
                                                               const uint8_t* __restrict__ scales, int64_t ld_scales,
                                                               const Rows rows, const CachePages pages,
@@ -182,21 +199,18 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const uint8_t* __r
   pdl_wait_predecessor();
   Unit u[kUnits];
   locate(u, rows, pages, err);
-  uint2 x[kUnits];
+  uint4 x[kUnits];
   uint32_t s[kUnits];
 #pragma unroll
   for (int i = 0; i < kUnits; ++i)
     if (u[i].at >= 0) {
-      x[i] = __ldg(reinterpret_cast<const uint2*>(codes + u[i].at * ld_codes + u[i].col * 8));
-      s[i] = __ldg(scales + u[i].at * ld_scales + (u[i].col >> 2));
+      x[i] = __ldg(reinterpret_cast<const uint4*>(codes + u[i].at * ld_codes + u[i].col * kUnitCols));
+      s[i] = __ldg(scales + u[i].at * ld_scales + (u[i].col >> 1));
     }
 #pragma unroll
   for (int i = 0; i < kUnits; ++i)
-    if (u[i].at >= 0) {
-      const uint32_t s2 = scale_bf16x2(s[i]);
-      const uint2 a = e4m3x4_scaled(x[i].x, s2), b = e4m3x4_scaled(x[i].y, s2);
-      dst[u[i].row * ld_dst_v + u[i].col] = make_uint4(a.x, a.y, b.x, b.y);
-    }
+    if (u[i].at >= 0)
+      store16<WIDE>(dst + u[i].row * ld_dst_v + u[i].col * 2, e4m3x16_scaled(x[i], scale_bf16x2(s[i])));
 }
 
 }  // namespace
@@ -227,21 +241,23 @@ kalm_status check_cache_args(const char* what, const void* bf, int64_t ld_bf, co
     return fail(KALM_ERR_INVALID_ARG, "%s: NULL pointer", what);
   if (!aligned16(bf) || !aligned16(codes))
     return fail(KALM_ERR_INVALID_ARG, "%s: values and codes must be 16-byte aligned", what);
-  if ((total_rows * static_cast<__int128>(width) / 8 + 32 * kUnits) / (kThreads * kUnits) > INT32_MAX - 1)
+  if (total_rows * static_cast<__int128>(width) / kUnitCols / (kThreads * kUnits) > INT32_MAX - 1)
     return fail(KALM_ERR_INVALID_ARG, "%s: too many values (%lld rows of %d)", what, (long long)total_rows, width);
   return KALM_OK;
 }
 
 Rows make_rows(const int64_t* row_off, const int32_t* first_row, int32_t n_docs, int64_t total_rows, int32_t width) {
-  return Rows{row_off, first_row, n_docs, total_rows, width / 8};
+  return Rows{row_off, first_row, n_docs, total_rows, width / kUnitCols};
 }
 
 CachePages make_pages(const int32_t* page_table, int64_t ld_table, int32_t page_rows, int64_t n_pages) {
   return CachePages{page_table, ld_table, n_pages, __builtin_ctz(static_cast<unsigned>(page_rows))};
 }
 
+bool rows_aligned32(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0 && ld % 16 == 0; }
+
 dim3 cache_grid(int64_t total_rows, int32_t width) {
-  const int64_t units = total_rows * (width / 8);
+  const int64_t units = total_rows * (width / kUnitCols);
   return dim3(static_cast<unsigned>((units + kThreads * kUnits - 1) / (kThreads * kUnits)));
 }
 
@@ -257,7 +273,7 @@ extern "C" kalm_status kalm_cache_write(const kalm_bf16* src, int64_t ld_src, co
   if (st != KALM_OK) return st;
   if ((st = ensure_device(nullptr)) != KALM_OK) return st;
   if (n_docs == 0 || total_rows == 0) return KALM_OK;
-  return check_cuda(launch_pdl(cache_write_kernel, cache_grid(total_rows, width), dim3(kThreads), 0,
+  return check_cuda(launch_pdl(rows_aligned32(src, ld_src) ? cache_write_kernel<true> : cache_write_kernel<false>, cache_grid(total_rows, width), dim3(kThreads), 0,
                                static_cast<cudaStream_t>(stream), reinterpret_cast<const uint4*>(src), ld_src / 8,
                                make_rows(row_off, first_row, n_docs, total_rows, width),
                                make_pages(page_table, ld_table, page_rows, n_pages), codes, ld_codes, scales,
@@ -275,7 +291,7 @@ extern "C" kalm_status kalm_cache_read(const uint8_t* codes, int64_t ld_codes, c
   if (st != KALM_OK) return st;
   if ((st = ensure_device(nullptr)) != KALM_OK) return st;
   if (n_docs == 0 || total_rows == 0) return KALM_OK;
-  return check_cuda(launch_pdl(cache_read_kernel, cache_grid(total_rows, width), dim3(kThreads), 0,
+  return check_cuda(launch_pdl(rows_aligned32(dst, ld_dst) ? cache_read_kernel<true> : cache_read_kernel<false>, cache_grid(total_rows, width), dim3(kThreads), 0,
                                static_cast<cudaStream_t>(stream), codes, ld_codes, scales, ld_scales,
                                make_rows(row_off, first_row, n_docs, total_rows, width),
                                make_pages(page_table, ld_table, page_rows, n_pages), reinterpret_cast<uint4*>(dst),

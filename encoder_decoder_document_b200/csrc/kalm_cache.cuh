@@ -13,6 +13,7 @@
 #include <cuda_fp8.h>
 
 #include "kalm.h"
+#include "kalm_ptx.cuh"
 
 namespace kalm {
 
@@ -46,7 +47,7 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two) {
 }
 
 // The bf16 pair (2^(b - 127), 2^(b - 127)) of a scale byte b in [1, 254].
-__device__ __forceinline__ uint32_t scale_bf16x2(uint32_t b) { return (b << 7) | (b << 23); }
+__device__ __forceinline__ uint32_t scale_bf16x2(uint32_t b) { return b * 0x00800080u; }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   const __nv_bfloat162 r =
@@ -58,6 +59,13 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint2 e4m3x4_scaled(uint32_t word, uint32_t scale2) {
   return make_uint2(mul_bf16x2(e4m3x2_to_bf16x2(word & 0xffffu), scale2),
                     mul_bf16x2(e4m3x2_to_bf16x2(word >> 16), scale2));
+}
+
+// Sixteen codes times their scale, as eight bf16 pairs; exact.
+__device__ __forceinline__ Words8 e4m3x16_scaled(const uint4& x, uint32_t scale2) {
+  const uint2 a = e4m3x4_scaled(x.x, scale2), b = e4m3x4_scaled(x.y, scale2);
+  const uint2 c = e4m3x4_scaled(x.z, scale2), d = e4m3x4_scaled(x.w, scale2);
+  return Words8{{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y}};
 }
 
 }  // namespace kalm

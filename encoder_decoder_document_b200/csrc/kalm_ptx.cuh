@@ -396,6 +396,27 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// ---------------------------------------------------------------- 32-byte global accesses
+// Eight 32-bit words of a 32-byte aligned address in one instruction.
+struct Words8 {
+  uint32_t w[8];
+};
+
+__device__ __forceinline__ Words8 ldg_words8(const void* p) {
+  Words8 v;
+  asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]), "=r"(v.w[6]),
+                 "=r"(v.w[7])
+               : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ void stg_words8(void* p, const Words8& v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v.w[0]), "r"(v.w[1]), "r"(v.w[2]),
+               "r"(v.w[3]), "r"(v.w[4]), "r"(v.w[5]), "r"(v.w[6]), "r"(v.w[7])
+               : "memory");
+}
+
 // ---------------------------------------------------------------- cross-CTA flags
 // gpu-scope acquire load / release add on a global counter (the producer-consumer
 // hand-off between CTAs of one launch).

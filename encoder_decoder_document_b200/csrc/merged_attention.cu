@@ -42,11 +42,8 @@
 //     the S products, warp 11 the P V products.  With two issuing threads, S of the
 //     next tiles goes out while P V waits for the softmax, so the tensor pipe does
 //     not idle behind one thread's waits.
-//   * With the cross K/V in an 8-bit cache (kalm_merged_attention_cache) four more warps,
-//     12-15, take the place of the TMA copies of the cross tiles: see CacheCross below.
 #include <cmath>
 #include <mutex>
-#include <type_traits>
 
 #include "kalm.h"
 #include "kalm_cache.cuh"
@@ -84,6 +81,7 @@ struct AttnParams {
   const int64_t* in_off;  // first q / self-K/V row of each document; NULL: q_off
   int last_only;          // compute only the query tile holding each document's last row
   const int64_t* pool_off;
+  int cross_pad;          // rows between two documents' cross rows (0: packed)
   __nv_bfloat16* out;
   float* lse;
   int64_t ldo;
@@ -132,6 +130,7 @@ __device__ __forceinline__ Item make_item(const AttnParams& p, int w) {
   it.t = p.last_only ? (it.Lq > 0 ? (it.Lq - 1) / p.P : 0) : p.tiles_per_doc - 1 - w / per_t;
   it.c0 = p.pool_off[it.d];
   it.Nc = static_cast<int>(p.pool_off[it.d + 1] - it.c0);
+  it.c0 += static_cast<int64_t>(it.d) * p.cross_pad;
   it.pos0 = it.t * p.P;
   it.pos1 = min(it.pos0 + p.P, it.Lq);
   it.n_self = it.pos0 < it.Lq ? (it.pos1 + kBKV - 1) / kBKV : 0;
@@ -421,217 +420,12 @@ __device__ __forceinline__ void out_proj_phase(const AttnParams& p, const ProjPa
   }
 }
 
-// ------------------------------------------------------------------------------
-// Where the cross K/V tiles come from.  TmaCross: bf16 rows, one TMA box a tile.
-// CacheCross: rows of an 8-bit cache, in pages.  Four warps widen each 64-row tile from
-// e4m3 codes to the bf16 values they stand for (exact) and write it where the TMA would
-// have put it, so that the rest of the kernel is the same.  Sixteen lanes take one
-// row (16 codes each), so a warp's load is two 256-byte runs whatever the pages'
-// order; the codes of the tile after the one being widened are loaded into the registers
-// that the widening frees, which hides their latency behind it.  Rows past the document's
-// last are written as zeros, those of the last self V tile too (a neighbouring document's
-// NaN would otherwise come through as 0 * NaN).
-struct TmaCross {};
-struct CacheCross {
-  const uint8_t* k_codes;
-  const uint8_t* v_codes;
-  const uint8_t* k_scales;
-  const uint8_t* v_scales;
-  int64_t ld_codes, ld_scales;
-  CachePages pages;
-  const __nv_bfloat16* v_self;
-  int64_t ld_self, total_in;  // rows of v_self
-};
-
-constexpr int kCacheWarp = 12;                       // first of the four widening warps
-constexpr int kCacheThreads = kThreads + 4 * 32;
-// The self tiles of an item that hold rows past the document's end: at most the last one.
-__device__ __forceinline__ bool self_tail(const Item& it, int j) { return j < it.n_self && (j + 1) * kBKV > it.Lq; }
-
-// One tile of the CTA's sequence, as the widening warps see it.
-struct TileRef {
-  int64_t row0;  // self tiles: first row of v_self; cross tiles: first row within the document
-  int d, g;
-  int valid;     // rows of the document in the tile
-  int kind;      // 0: filled by TMA; 1: self V tail; 2: cross; -1: no further tile
-  int32_t page;  // lanes 0..7: page of the tile's 8-row block `lane` (cross tiles), -1: none
-};
-
-__device__ __forceinline__ void widen_tiles(const AttnParams& p, const CacheCross& cc, uint8_t* sK, uint8_t* sV,
-                                            uint64_t* bar_k, uint64_t* bar_v, uint64_t* bar_s, uint64_t* bar_pv,
-                                            volatile int* abort_flag) {
-  const int w = (threadIdx.x >> 5) - kCacheWarp, lane = threadIdx.x & 31;
-  const int c = lane & 15;             // 16-column slice of the head
-  const int r_in = 2 * w + (lane >> 4);  // this lane's row in every 8-row block
-  const int64_t block_mask = (int64_t{1} << cc.pages.shift) - 1;
-
-  // ---- the CTA's tiles, in the order of every other role
-  int pass = 0, wc = item_at(p, 0), j = 0;
-  Item it = load_item(p, wc), nxt{};
-  int wn = kNoMore;
-  if (wc != kNoMore) {
-    wn = item_at(p, 1);
-    nxt = load_item(p, wn);
-  }
-  auto next_tile = [&]() {
-    TileRef r{};
-    while (wc != kNoMore && j >= it.nt) {
-      it = nxt;
-      wc = wn;
-      j = 0;
-      ++pass;
-      if (wc != kNoMore) {
-        wn = item_at(p, pass + 1);
-        nxt = load_item(p, wn);
-      }
-    }
-    if (wc == kNoMore) {
-      r.kind = -1;
-      return r;
-    }
-    r.d = it.d;
-    r.g = it.g;
-    r.page = -1;
-    if (j < it.n_self) {
-      r.kind = self_tail(it, j) ? 1 : 0;
-      r.row0 = it.qi + j * kBKV;
-      r.valid = min(kBKV, it.Lq - j * kBKV);
-    } else {
-      r.kind = 2;
-      r.row0 = static_cast<int64_t>(j - it.n_self) * kBKV;
-      r.valid = static_cast<int>(min(static_cast<int64_t>(kBKV), it.Nc - r.row0));
-      if (lane < kBKV / 8 && lane * 8 < r.valid) {
-        const int64_t at = (r.row0 + lane * 8) >> cc.pages.shift;
-        if (at < cc.pages.ld) r.page = __ldg(cc.pages.table + r.d * cc.pages.ld + at);
-      }
-    }
-    ++j;
-    return r;
-  };
-
-  uint4 buf[kBKV / 8];
-  uint32_t sc[kBKV / 8];
-  // this lane's codes and scale of row block b of a cross tile
-  auto load_block = [&](const TileRef& r, bool v, int b) {
-    const int64_t page = __shfl_sync(0xffffffffu, r.page, b);
-    const int row = 8 * b + r_in;
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    uint32_t s = 0;
-    if (row < r.valid) {
-      if (page >= 0 && page < cc.pages.n_pages) {
-        const int64_t at = (page << cc.pages.shift) + ((r.row0 + row) & block_mask);
-        x = __ldg(reinterpret_cast<const uint4*>((v ? cc.v_codes : cc.k_codes) + at * cc.ld_codes + r.g * kD) + c);
-        s = __ldg((v ? cc.v_scales : cc.k_scales) + at * cc.ld_scales + r.g * (kD / kCacheGroup) + (c >> 1));
-      } else if (c == 0 && !v) {
-        record_error(p.err, kErrDeviceArg | kSiteAttention);
-      }
-    }
-    buf[b] = x;
-    sc[b] = s;
-  };
-  // shared-memory place of this lane's 16 columns of row block b; unit h is its half of 8 columns
-  auto unit_at = [&](uint8_t* tile, int b, int h) {
-    const int row = 8 * b + r_in;
-    return reinterpret_cast<uint4*>(tile + (c >> 2) * kKVSlab + row * 128 + ((((c & 3) * 2 + h) ^ (row & 7)) << 4));
-  };
-  auto widen_block = [&](uint8_t* tile, int b) {
-    const uint32_t s2 = scale_bf16x2(sc[b]);
-    const uint2 a0 = e4m3x4_scaled(buf[b].x, s2), a1 = e4m3x4_scaled(buf[b].y, s2);
-    const uint2 a2 = e4m3x4_scaled(buf[b].z, s2), a3 = e4m3x4_scaled(buf[b].w, s2);
-    const uint4 lo = make_uint4(a0.x, a0.y, a1.x, a1.y), hi = make_uint4(a2.x, a2.y, a3.x, a3.y);
-    // lanes of odd 64-column slabs store their halves in the other order: eight lanes then
-    // write eight different 16-byte bank groups
-    const int odd = (c >> 2) & 1;
-    *unit_at(tile, b, odd) = odd ? hi : lo;
-    *unit_at(tile, b, odd ^ 1) = odd ? lo : hi;
-  };
-  auto give_up = [&]() {
-    if (lane == 0) record_error(p.err, kErrTimeout | kSiteAttention);
-    *abort_flag = 1;
-  };
-  auto publish = [&](uint64_t* bar) {
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar);
-  };
-
-  TileRef cur = next_tile();
-  if (cur.kind == 2)
-#pragma unroll
-    for (int b = 0; b < kBKV / 8; ++b) load_block(cur, false, b);
-  for (uint32_t J = 0; cur.kind >= 0; ++J) {
-    const int s = J & 1;
-    const TileRef next = next_tile();  // its page numbers are on their way during this tile
-    // K: its slot is free once S_{J-2} is done.  Every tile's barriers are waited on and arrived at,
-    // also where nothing is written.
-    bool ok = J < 2 || mbar_wait(&bar_s[s], ((J - 2) >> 1) & 1, p.wait_ns);
-    if (__any_sync(0xffffffffu, !ok || *abort_flag)) {  // one vote: the whole warp leaves or none
-      give_up();
-      break;
-    }
-    if (cur.kind == 2) {
-      uint8_t* tile = sK + s * kKVBytes;
-#pragma unroll
-      for (int b = 0; b < kBKV / 8; ++b) {
-        widen_block(tile, b);
-        load_block(cur, true, b);
-      }
-    }
-    publish(&bar_k[s]);
-    ok = J < 2 || mbar_wait(&bar_pv[s], ((J - 2) >> 1) & 1, p.wait_ns);
-    if (__any_sync(0xffffffffu, !ok || *abort_flag)) {  // one vote: the whole warp leaves or none
-      give_up();
-      break;
-    }
-    uint8_t* tile = sV + s * kKVBytes;
-    if (cur.kind == 2) {
-#pragma unroll
-      for (int b = 0; b < kBKV / 8; ++b) {
-        widen_block(tile, b);
-        if (next.kind == 2) load_block(next, false, b);
-      }
-      publish(&bar_v[s]);
-    } else {
-      if (cur.kind == 1) {
-        const __nv_bfloat16* src = cc.v_self + cur.row0 * cc.ld_self + static_cast<int64_t>(cur.g) * kD + c * 16;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint4 x[4][2];
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int row = 8 * (4 * q + b) + r_in;
-              x[b][h] = make_uint4(0u, 0u, 0u, 0u);
-              if (row < cur.valid && cur.row0 + row < cc.total_in) x[b][h] = *reinterpret_cast<const uint4*>(src + row * cc.ld_self + h * 8);
-            }
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) *unit_at(tile, 4 * q + b, h) = x[b][h];
-        }
-      }
-      publish(&bar_v[s]);
-      if (next.kind == 2)
-#pragma unroll
-        for (int b = 0; b < kBKV / 8; ++b) load_block(next, false, b);
-    }
-    cur = next;
-  }
-}
-
-template <bool FUSED, typename Cross>
-__global__ void __launch_bounds__(std::is_same<Cross, CacheCross>::value ? kCacheThreads : kThreads, 1)
+template <bool FUSED>
+__global__ void __launch_bounds__(kThreads, 1)
     merged_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_ks,
                             const __grid_constant__ CUtensorMap tm_vs, const __grid_constant__ CUtensorMap tm_kc,
                             const __grid_constant__ CUtensorMap tm_vc, const __grid_constant__ CUtensorMap tm_oa,
-                            const __grid_constant__ CUtensorMap tm_wo, const AttnParams p, const ProjParams f,
-                            const Cross cross) {
-  constexpr bool CACHE = std::is_same<Cross, CacheCross>::value;
-  // Arrivals that complete a K or V tile.  With a cache both the TMA thread and the four widening warps
-  // arrive for every tile, whoever fills it, so that neither can fall more than one phase behind the
-  // barriers that it waits on (a parity wait would then be ambiguous).
-  constexpr int kFills = CACHE ? 5 : 1;
+                            const __grid_constant__ CUtensorMap tm_wo, const AttnParams p, const ProjParams f) {
   pdl_launch_dependents();
   pdl_wait_predecessor();  // q/K/V come from the previous kernel; offsets are read by every role
 
@@ -669,8 +463,8 @@ __global__ void __launch_bounds__(std::is_same<Cross, CacheCross>::value ? kCach
     mbar_init(bar_q, 1);
     mbar_init(bar_qfree, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar_k[i], kFills);
-      mbar_init(&bar_v[i], kFills);
+      mbar_init(&bar_k[i], 1);
+      mbar_init(&bar_v[i], 1);
       mbar_init(&bar_s[i], 1);
       mbar_init(&bar_p[i], kSoftmaxThreads / 2);  // one warp group writes each tile's P
       mbar_init(&bar_sfree[i], kSoftmaxThreads / 2);
@@ -712,9 +506,7 @@ __global__ void __launch_bounds__(std::is_same<Cross, CacheCross>::value ? kCach
     *abort_flag = 1;
   };
 
-  if (CACHE && warp >= kCacheWarp) {
-    if constexpr (CACHE) widen_tiles(p, cross, sK, sV, bar_k, bar_v, bar_s, bar_pv, abort_flag);
-  } else if (warp == kTmaWarp || warp == kTmaWarpV) {
+  if (warp == kTmaWarp || warp == kTmaWarpV) {
     // ------------------------------------------------------------ TMA producers (Q+K, V)
     if (lane == 0) {
       const bool is_v = warp == kTmaWarpV;
@@ -758,13 +550,8 @@ __global__ void __launch_bounds__(std::is_same<Cross, CacheCross>::value ? kCach
             ok = false;
             break;
           }
-          // (with a cache, the widening warps fill the cross tiles and the self V tail)
-          if (!CACHE || (self && !(is_v && self_tail(it, j)))) {
-            mbar_arrive_expect_tx(&bar_full[s], kKVBytes);
-            tma_load_3d(ring + s * kKVBytes, m, &bar_full[s], 0, row, it.g * 4);
-          } else {
-            mbar_arrive(&bar_full[s]);
-          }
+          mbar_arrive_expect_tx(&bar_full[s], kKVBytes);
+          tma_load_3d(ring + s * kKVBytes, m, &bar_full[s], 0, row, it.g * 4);
           last_j = J;
           if (!is_v && j == 0 && nxt.nt > 0) {
             // next item's Q as soon as this item's Q is in tensor memory
@@ -1304,17 +1091,12 @@ __global__ void __launch_bounds__(kSchedThreads) attention_schedule_kernel(const
 
 kalm_status setup_attention_kernels() {
   kalm_status st = check_cuda(
-      cudaFuncSetAttribute(merged_attention_kernel<false, TmaCross>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kSmem),
+      cudaFuncSetAttribute(merged_attention_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
       "cudaFuncSetAttribute(merged_attention_kernel)");
   if (st != KALM_OK) return st;
-  st = check_cuda(cudaFuncSetAttribute(merged_attention_kernel<false, CacheCross>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
-                  "cudaFuncSetAttribute(merged_attention_kernel<cache>)");
-  if (st != KALM_OK) return st;
-  return check_cuda(cudaFuncSetAttribute(merged_attention_kernel<true, TmaCross>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
-                    "cudaFuncSetAttribute(merged_attention_kernel<fused>)");
+  return check_cuda(
+      cudaFuncSetAttribute(merged_attention_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
+      "cudaFuncSetAttribute(merged_attention_kernel<fused>)");
 }
 
 }  // namespace kalm
@@ -1333,7 +1115,7 @@ struct OutProj {
   int32_t* sync;
 };
 
-// The checks of a call's sizes and pointers that need no device.
+// The checks of a call's sizes and pointers, which need no device.
 kalm_status check_attention(const kalm_bf16* q, int64_t ldq, const kalm_bf16* k_self, const kalm_bf16* v_self,
                             int64_t ld_self, const kalm_bf16* k_cross, const kalm_bf16* v_cross, int64_t ld_cross,
                             const int64_t* q_off, const int64_t* in_off, int64_t total_in, const int64_t* pool_off,
@@ -1347,7 +1129,7 @@ kalm_status check_attention(const kalm_bf16* q, int64_t ldq, const kalm_bf16* k_
   const int G = n_q / n_kv;
   if (kBM % G) return fail(KALM_ERR_UNSUPPORTED, "kalm_merged_attention: n_q/n_kv=%d must divide 128", G);
   if (!(scale > 0.f) || !std::isfinite(scale)) return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention: bad scale");
-  if (n_docs == 0 || max_q == 0 || total_q == 0) return KALM_OK;  // nothing to compute
+  if (n_docs == 0 || max_q == 0 || total_q == 0) return KALM_OK;
   if (!q || !k_self || !v_self || !out || !q_off || !pool_off || (total_pool > 0 && (!k_cross || !v_cross)))
     return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention: NULL pointer");
   if (ldq % 8 || ld_self % 8 || ld_cross % 8 || ldo % 8 || ldq < (int64_t)n_q * kD || ld_self < (int64_t)n_kv * kD ||
@@ -1363,14 +1145,14 @@ kalm_status check_attention(const kalm_bf16* q, int64_t ldq, const kalm_bf16* k_
   return KALM_OK;
 }
 
-// `cache`: the cross K/V come from an 8-bit cache (k_cross, v_cross NULL, total_pool 0); NULL: from bf16 rows.
+// `cross_pad`: rows between two documents' cross rows (0 where they are packed by pool_off).
 kalm_status launch_attention(const kalm_bf16* q, int64_t ldq, const kalm_bf16* k_self, const kalm_bf16* v_self,
                              int64_t ld_self, const kalm_bf16* k_cross, const kalm_bf16* v_cross, int64_t ld_cross,
                              const int64_t* q_off, const int64_t* in_off, int64_t total_in, const int64_t* pool_off,
                              int32_t n_docs, int32_t max_q, int64_t total_q, int64_t total_pool, int32_t n_q,
                              int32_t n_kv, int32_t head_dim, float scale, int32_t last_tile_only,
                              const int32_t* order, kalm_bf16* out, int64_t ldo, float* lse, const OutProj* op,
-                             const CacheCross* cache, kalm_stream_t stream) {
+                             kalm_stream_t stream, int32_t cross_pad = 0) {
   kalm_status st = ensure_device(nullptr);
   if (st != KALM_OK) return st;
   st = check_attention(q, ldq, k_self, v_self, ld_self, k_cross, v_cross, ld_cross, q_off, in_off, total_in, pool_off,
@@ -1412,6 +1194,7 @@ kalm_status launch_attention(const kalm_bf16* q, int64_t ldq, const kalm_bf16* k
   prm.in_off = in_off;
   prm.last_only = last_tile_only ? 1 : 0;
   prm.pool_off = pool_off;
+  prm.cross_pad = cross_pad;
   prm.out = reinterpret_cast<__nv_bfloat16*>(out);
   prm.lse = lse;
   prm.ldo = ldo;
@@ -1433,16 +1216,10 @@ kalm_status launch_attention(const kalm_bf16* q, int64_t ldq, const kalm_bf16* k
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (sms <= 0) sms = 148;
   const int64_t grid = items < sms ? items : sms;  // persistent: one CTA per SM
-  if (cache) {
-    return check_cuda(launch_pdl(merged_attention_kernel<false, CacheCross>, dim3(static_cast<unsigned>(grid)),
-                                 dim3(kCacheThreads), kSmem, static_cast<cudaStream_t>(stream), tq, tks, tvs, tkc, tvc,
-                                 tq, tq, prm, ProjParams{}, *cache),
-                      "launch merged_attention_kernel<cache>");
-  }
   if (!op) {
-    return check_cuda(launch_pdl(merged_attention_kernel<false, TmaCross>, dim3(static_cast<unsigned>(grid)),
-                                 dim3(kThreads), kSmem, static_cast<cudaStream_t>(stream), tq, tks, tvs, tkc, tvc, tq,
-                                 tq, prm, ProjParams{}, TmaCross{}),
+    return check_cuda(launch_pdl(merged_attention_kernel<false>, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
+                                 kSmem, static_cast<cudaStream_t>(stream), tq, tks, tvs, tkc, tvc, tq, tq, prm,
+                                 ProjParams{}),
                       "launch merged_attention_kernel");
   }
   // fused output projection: A = O rows of a document (the `out` written above), B = Wo
@@ -1470,9 +1247,8 @@ kalm_status launch_attention(const kalm_bf16* q, int64_t ldq, const kalm_bf16* k
   if (otiles + grid > INT32_MAX) return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention_out_proj: too many tiles");
   fp.n_otiles = static_cast<int>(otiles);
   fp.sync = op->sync;
-  return check_cuda(launch_pdl(merged_attention_kernel<true, TmaCross>, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
-                               kSmem, static_cast<cudaStream_t>(stream), tq, tks, tvs, tkc, tvc, toa, two, prm, fp,
-                               TmaCross{}),
+  return check_cuda(launch_pdl(merged_attention_kernel<true>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmem,
+                               static_cast<cudaStream_t>(stream), tq, tks, tvs, tkc, tvc, toa, two, prm, fp),
                     "launch merged_attention_kernel<fused>");
 }
 
@@ -1488,7 +1264,92 @@ extern "C" kalm_status kalm_merged_attention(const kalm_bf16* q, int64_t ldq, co
                                              int64_t ldo, float* lse, kalm_stream_t stream) {
   return launch_attention(q, ldq, k_self, v_self, ld_self, k_cross, v_cross, ld_cross, q_off, in_off, total_in,
                           pool_off, n_docs, max_q, total_q, total_pool, n_q, n_kv, head_dim, scale, last_tile_only,
-                          order, out, ldo, lse, nullptr, nullptr, stream);
+                          order, out, ldo, lse, nullptr, stream);
+}
+
+// ----------------------------------------------------------------------------------
+// Attention over an 8-bit cache, in two launches: the cached K/V rows of the call's documents are widened to the
+// bf16 values they stand for (exactly) into the caller's workspace, and the attention kernel reads them from
+// there with its TMA copies, out of L2 as far as they fit.
+//
+// Widening inside the attention kernel was built and measured: eight more warps wrote each tile from its codes to
+// shared memory, no workspace.  A layer of 100 documents x 128 positions (4 query tiles a document, so every
+// cached tile is widened 4 times) took 55 us against 38 us for the two launches, 100 documents x 256 positions
+// of 8 heads 157 us against 116 us, one position per document 19 us against 15 us: a tile's widening takes
+// about 3,500 cycles of a warp pair on the schedulers that the softmax also needs, more than the 1,700
+// cycles in which the bf16 kernel consumes a tile.
+//
+// Widening kernel: one block per (document, 64 rows, K or V, head).  Bound by latency at these sizes (three
+// dependent loads: the document's offsets, its pages, the codes), by memory for large ones (3 + 1/32 bytes a
+// value).  A warp takes eight rows, two at a time, 16
+// codes a lane; rows up to the next multiple of 64 become zeros, so that
+// the attention's last tile of a document multiplies its masked probabilities with finite values.
+namespace kalm {
+namespace {
+
+constexpr int kWidenThreads = 256;
+constexpr int kCrossPad = 64;  // between two documents' rows: room for the last tile's zeros
+
+struct WidenParams {
+  const uint8_t* codes[2];   // K, V
+  const uint8_t* scales[2];
+  int64_t ld_codes, ld_scales;
+  CachePages pages;
+  const int64_t* pool_off;
+  __nv_bfloat16* ws;         // [ws_rows][2][n_kv][256]
+  int64_t ws_rows;
+  int n_kv;
+  uint32_t* err;
+};
+
+__global__ void __launch_bounds__(kWidenThreads) cache_widen_kernel(const WidenParams p) {
+  pdl_launch_dependents();
+  pdl_wait_predecessor();
+  constexpr int kRows = kBKV / (kWidenThreads / 32);  // rows of a warp
+  const int d = blockIdx.y, g = blockIdx.z >> 1, v = blockIdx.z & 1;
+  const int64_t c0 = __ldg(p.pool_off + d);
+  const int64_t nc = __ldg(p.pool_off + d + 1) - c0;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kBKV;
+  if (r0 >= nc) return;
+  const int64_t to = c0 + static_cast<int64_t>(d) * kCrossPad;  // the document's first workspace row
+  if (c0 < 0 || to + r0 + kBKV > p.ws_rows) {
+    if (threadIdx.x == 0) record_error(p.err, kErrDeviceArg | kSiteAttention);
+    return;
+  }
+  const int lane = threadIdx.x & 31, half = lane >> 4, c = lane & 15;
+  const int64_t first = r0 + (threadIdx.x >> 5) * kRows;  // the warp's rows
+  // lanes 0 .. kRows - 1 look up a row each
+  int64_t mine = -1;
+  if (lane < kRows && first + lane < nc) {
+    mine = cache_row(p.pages, d, first + lane);
+    if (mine < 0) record_error(p.err, kErrDeviceArg | kSiteAttention);
+  }
+  const uint8_t* const codes = p.codes[v] + g * kD + c * 16;
+  const uint8_t* const scales = p.scales[v] + g * (kD / kCacheGroup) + (c >> 1);
+  uint4 x[kRows / 2];
+  uint32_t s[kRows / 2];
+#pragma unroll
+  for (int i = 0; i < kRows / 2; ++i) {
+    const int64_t at = __shfl_sync(0xffffffffu, mine, 2 * i + half);
+    x[i] = make_uint4(0u, 0u, 0u, 0u);
+    s[i] = 0;
+    if (at >= 0) {
+      x[i] = __ldg(reinterpret_cast<const uint4*>(codes + at * p.ld_codes));
+      s[i] = __ldg(scales + at * p.ld_scales);
+    }
+  }
+  __nv_bfloat16* const dst = p.ws + ((to + first + half) * 2 + v) * p.n_kv * kD + g * kD + c * 16;
+#pragma unroll
+  for (int i = 0; i < kRows / 2; ++i)
+    stg_words8(dst + static_cast<int64_t>(i) * 4 * p.n_kv * kD, e4m3x16_scaled(x[i], scale_bf16x2(s[i])));
+}
+
+}  // namespace
+}  // namespace kalm
+
+extern "C" int64_t kalm_merged_attention_cache_rows(int64_t total_pool, int32_t n_docs) {
+  if (total_pool < 0 || n_docs < 0) return -1;
+  return total_pool + static_cast<int64_t>(n_docs) * kCrossPad;
 }
 
 extern "C" kalm_status kalm_merged_attention_cache(
@@ -1497,31 +1358,54 @@ extern "C" kalm_status kalm_merged_attention_cache(
     int64_t ld_scales, const int32_t* page_table, int64_t ld_table, int32_t page_rows, int64_t n_pages,
     const int64_t* q_off, const int64_t* in_off, int64_t total_in, const int64_t* pool_off, int32_t n_docs,
     int32_t max_q, int64_t total_q, int32_t n_q, int32_t n_kv, int32_t head_dim, float scale, int32_t last_tile_only,
-    const int32_t* order, kalm_bf16* out, int64_t ldo, float* lse, kalm_stream_t stream) {
-  kalm_status st = check_attention(q, ldq, k_self, v_self, ld_self, nullptr, nullptr, 0, q_off, in_off, total_in,
-                                   pool_off, n_docs, max_q, total_q, 0, n_q, n_kv, head_dim, scale, out, ldo);
+    const int32_t* order, kalm_bf16* workspace, int64_t workspace_rows, kalm_bf16* out, int64_t ldo, float* lse,
+    kalm_stream_t stream) {
+  const int64_t width = static_cast<int64_t>(n_kv) * kD;
+  const int64_t rows = ld_table > 0 ? workspace_rows : 0;  // no pages, nothing cached
+  kalm_status st = check_attention(q, ldq, k_self, v_self, ld_self, workspace, workspace, 2 * width, q_off, in_off,
+                                   total_in, pool_off, n_docs, max_q, total_q, rows, n_q, n_kv, head_dim, scale, out,
+                                   ldo);
   if (st != KALM_OK) return st;
   if (page_rows < KALM_CACHE_MIN_PAGE_ROWS || page_rows > KALM_CACHE_MAX_PAGE_ROWS || (page_rows & (page_rows - 1)))
     return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention_cache: page_rows=%d is not a power of two in [%d, %d]",
                 page_rows, KALM_CACHE_MIN_PAGE_ROWS, KALM_CACHE_MAX_PAGE_ROWS);
-  if (n_pages < 0 || n_pages > INT32_MAX || ld_table < 0)
-    return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention_cache: n_pages=%lld ld_table=%lld", (long long)n_pages,
-                (long long)ld_table);
-  if (n_docs > 0 && max_q > 0 && total_q > 0) {
-    if ((n_pages > 0 && (!k_codes || !v_codes || !k_scales || !v_scales)) || (ld_table > 0 && !page_table))
+  if (n_pages < 0 || n_pages > INT32_MAX || ld_table < 0 || ld_table > INT32_MAX / page_rows || workspace_rows < 0)
+    return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention_cache: n_pages=%lld ld_table=%lld workspace_rows=%lld",
+                (long long)n_pages, (long long)ld_table, (long long)workspace_rows);
+  const bool any = n_docs > 0 && max_q > 0 && total_q > 0;
+  if (any && ld_table > 0) {
+    if (!page_table || (n_pages > 0 && (!k_codes || !v_codes || !k_scales || !v_scales)))
       return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention_cache: NULL pointer");
-    const int64_t width = static_cast<int64_t>(n_kv) * kD;
+    if (workspace_rows == 0)
+      return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention_cache: no workspace");
+    if (reinterpret_cast<uintptr_t>(workspace) & 31u)
+      return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention_cache: the workspace must be 32-byte aligned");
     if (!aligned16(k_codes) || !aligned16(v_codes) || ld_codes % 16 || ld_codes < width ||
         ld_scales < width / kCacheGroup)
-      return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention_cache: codes must be 16-byte aligned, the strides "
-                  "(%lld, %lld) cover all heads", (long long)ld_codes, (long long)ld_scales);
+      return fail(KALM_ERR_INVALID_ARG,
+                  "kalm_merged_attention_cache: codes must be 16-byte aligned, the strides (%lld, a multiple of 16; "
+                  "%lld) cover all heads",
+                  (long long)ld_codes, (long long)ld_scales);
+    if (n_docs > 65535 || n_kv > 32767)
+      return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention_cache: n_docs=%d n_kv=%d", n_docs, n_kv);
   }
-  const CacheCross cache{k_codes, v_codes, k_scales, v_scales, ld_codes, ld_scales,
+  if ((st = ensure_device(nullptr)) != KALM_OK) return st;
+  if (any && ld_table > 0) {
+    const int64_t tiles = (ld_table * page_rows + kBKV - 1) / kBKV;  // of the longest document the table can hold
+    const WidenParams wp{{k_codes, v_codes}, {k_scales, v_scales}, ld_codes, ld_scales,
                          CachePages{page_table, ld_table, n_pages, __builtin_ctz(static_cast<unsigned>(page_rows))},
-                         reinterpret_cast<const __nv_bfloat16*>(v_self), ld_self, in_off ? total_in : total_q};
-  return launch_attention(q, ldq, k_self, v_self, ld_self, nullptr, nullptr, 0, q_off, in_off, total_in, pool_off,
-                          n_docs, max_q, total_q, 0, n_q, n_kv, head_dim, scale, last_tile_only, order, out, ldo, lse,
-                          nullptr, &cache, stream);
+                         pool_off, reinterpret_cast<__nv_bfloat16*>(workspace), workspace_rows, n_kv,
+                         device_error_word()};
+    st = check_cuda(launch_pdl(cache_widen_kernel,
+                               dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(n_docs),
+                                    static_cast<unsigned>(2 * n_kv)),
+                               dim3(kWidenThreads), 0, static_cast<cudaStream_t>(stream), wp),
+                    "launch cache_widen_kernel");
+    if (st != KALM_OK) return st;
+  }
+  return launch_attention(q, ldq, k_self, v_self, ld_self, workspace, workspace ? workspace + width : nullptr,
+                          2 * width, q_off, in_off, total_in, pool_off, n_docs, max_q, total_q, rows, n_q, n_kv,
+                          head_dim, scale, last_tile_only, order, out, ldo, lse, nullptr, stream, kCrossPad);
 }
 
 extern "C" int64_t kalm_attention_out_proj_sync_len(int32_t n_docs, int32_t max_q, int32_t hidden) {
@@ -1553,7 +1437,7 @@ extern "C" kalm_status kalm_merged_attention_out_proj(
   const OutProj op{w_o, ldw, x, ldx, hidden, sync};
   return launch_attention(q, ldq, k_self, v_self, ld_self, k_cross, v_cross, ld_cross, q_off, in_off, total_in,
                           pool_off, n_docs, max_q, total_q, total_pool, n_q, n_kv, head_dim, scale, 0, order, out, ldo,
-                          nullptr, &op, nullptr, stream);
+                          nullptr, &op, stream);
 }
 
 // ----------------------------------------------------------------------------------

@@ -481,8 +481,8 @@ kalm_status kalm_linear_rope(const kalm_bf16* x, int64_t ldx, const kalm_bf16* w
  * scales.  Documents may share pages where they are read.  codes: uint8
  * [n_pages * page_rows][ld_codes], 16-byte aligned, ld_codes a multiple of 16;
  * scales: uint8 [n_pages * page_rows][ld_scales].  A row whose place in the table
- * is missing or names no page in [0, n_pages) is skipped (it reads as zeros in the
- * attention) and flagged in the device error word.
+ * is missing or names no page in [0, n_pages) is skipped and flagged in the device
+ * error word.
  * ------------------------------------------------------------------------- */
 #define KALM_CACHE_GROUP 32
 #define KALM_CACHE_MIN_PAGE_ROWS 8
@@ -517,9 +517,10 @@ kalm_status kalm_cache_read(const uint8_t* codes, int64_t ld_codes, const uint8_
 /* kalm_merged_attention with the cross K/V read from an 8-bit cache: the same
  * softmax over [causal self rows ; cross rows 0..Nc[d]-1], where document d's
  * cross rows are the rows of its pages.  The keys and values are the stored
- * numbers exactly (they are bf16 numbers, widened on the way to the tensor
- * cores), so the result is that of kalm_merged_attention over the rows that
- * kalm_cache_read returns.  Same passages as kalm_merged_attention.
+ * numbers exactly, so the result is that of kalm_merged_attention over the rows
+ * that kalm_cache_read returns.  Same passages as kalm_merged_attention.  Two
+ * launches: the call's cached rows are widened to bf16 into the workspace, once for
+ * all their query tiles, and attended over from there.
  *
  * q .. total_in, max_q, total_q, n_q .. lse   as kalm_merged_attention (order from
  *          kalm_attention_schedule for the same offsets and sizes, or NULL)
@@ -528,11 +529,17 @@ kalm_status kalm_cache_read(const uint8_t* codes, int64_t ld_codes, const uint8_
  * k_scales, v_scales their scale bytes: head g at byte g * 8, common stride
  *          ld_scales
  * pool_off int64[n_docs + 1]: document d attends to its first Nc[d] = pool_off[d+1]
- *          - pool_off[d] cached rows
- * What belongs to other documents or lies behind a document's last row (self rows
- * or cached ones) has no influence, NaN and infinities included.  Within a
- * document, a NaN or infinity in a self V row reaches every decoder row of the
- * query tile (128 / (n_q / n_kv) positions) that holds a row which sees it. */
+ *          - pool_off[d] cached rows.  A row whose place in the table is missing or
+ *          names no page counts as a row of zeros and is flagged.
+ * workspace bf16 [workspace_rows][2 * n_kv * head_dim], 32-byte aligned, of at least
+ *          kalm_merged_attention_cache_rows(pool_off[n_docs], n_docs) rows (a
+ *          document that reaches past it is flagged); scratch, no contents are
+ *          kept from call to call.  Calls that overlap on the GPU need their own.
+ *          NULL with 0 rows where ld_table is 0 (nothing cached).
+ * What lies behind a document's last cached row has no influence, NaN and
+ * infinities included.  As with kalm_merged_attention, the self rows are to be
+ * finite: a NaN or infinity in a V row reaches the query tiles (128 / (n_q / n_kv)
+ * positions) that load its 64-row tile, those of the document before included. */
 kalm_status kalm_merged_attention_cache(const kalm_bf16* q, int64_t ldq, const kalm_bf16* k_self,
                                         const kalm_bf16* v_self, int64_t ld_self, const uint8_t* k_codes,
                                         const uint8_t* v_codes, int64_t ld_codes, const uint8_t* k_scales,
@@ -541,7 +548,12 @@ kalm_status kalm_merged_attention_cache(const kalm_bf16* q, int64_t ldq, const k
                                         const int64_t* in_off, int64_t total_in, const int64_t* pool_off,
                                         int32_t n_docs, int32_t max_q, int64_t total_q, int32_t n_q, int32_t n_kv,
                                         int32_t head_dim, float scale, int32_t last_tile_only, const int32_t* order,
-                                        kalm_bf16* out, int64_t ldo, float* lse, kalm_stream_t stream);
+                                        kalm_bf16* workspace, int64_t workspace_rows, kalm_bf16* out, int64_t ldo,
+                                        float* lse, kalm_stream_t stream);
+
+/* Rows of kalm_merged_attention_cache's workspace for total_pool cached rows of
+ * n_docs documents (total_pool + 64 n_docs), or -1 for negative sizes. */
+int64_t kalm_merged_attention_cache_rows(int64_t total_pool, int32_t n_docs);
 
 /* ---------------------------------------------------------------------------
  * The norms around a decoder block.

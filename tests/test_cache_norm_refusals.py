@@ -20,7 +20,7 @@ READ_ORDER = ("codes", "ld_codes", "scales", "ld_scales", "row_off", "n_docs", "
 ATTENTION = dict(q=A, ldq=1024, k_self=A, v_self=A, ld_self=256, k_codes=A, v_codes=A, ld_codes=512, k_scales=A, v_scales=A,
                  ld_scales=16, page_table=A, ld_table=3, page_rows=16, n_pages=7, q_off=A, in_off=None, total_in=40,
                  pool_off=A, n_docs=2, max_q=20, total_q=40, n_q=4, n_kv=1, head_dim=256, scale=0.0625, last=0,
-                 order=None, out=A, ldo=1024, lse=None, stream=None)
+                 order=None, workspace=A, workspace_rows=200, out=A, ldo=1024, lse=None, stream=None)
 NORM = dict(x=A, ldx=64, w=A, h=A, ldh=64, rows=3, width=64, eps=1e-6, off=0.0, stream=None)
 RESIDUAL = dict(y=A, ldy=64, x=A, ldx=64, w_post=A, gate=A, ld_gate=64, q_off=A, n_docs=2, scale=1.0, x_out=A, ldxo=64,
                 w_pre=A, h=2 * A, ldh=64, rows=3, width=64, eps=1e-6, off=0.0, stream=None)
@@ -46,7 +46,8 @@ def test_cache_calls_refuse(lib, bad):
     (dict(scale=0.0), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(q=None), 1), (dict(out=None), 1),
     (dict(q_off=None), 1), (dict(pool_off=None), 1), (dict(ldq=1020), 1), (dict(ldo=512), 1), (dict(ld_self=128), 1),
     (dict(k_codes=None), 1), (dict(v_scales=None), 1), (dict(page_table=None), 1), (dict(k_codes=A + 4), 1),
-    (dict(ld_codes=520), 1), (dict(ld_codes=240), 1), (dict(ld_scales=7), 1), (dict(page_rows=12), 1), (dict(page_rows=2048), 1),
+    (dict(ld_codes=520), 1), (dict(ld_codes=240), 1), (dict(ld_scales=7), 1), (dict(workspace=None), 1), (dict(workspace_rows=0), 1),
+    (dict(workspace_rows=-1), 1), (dict(workspace=A + 8), 1), (dict(workspace=A + 16), 1), (dict(n_docs=70000), 1), (dict(page_rows=12), 1), (dict(page_rows=2048), 1),
     (dict(n_pages=-1), 1), (dict(ld_table=-2), 1), (dict(in_off=A, total_in=0), 1), (dict(total_q=-1), 1),
 ], ids=str)
 def test_attention_refuses(lib, bad, status):
