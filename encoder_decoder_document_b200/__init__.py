@@ -32,8 +32,10 @@ CACHE_GROUP = 32  # KALM_CACHE_GROUP: columns of a cached row that share a scale
 
 
 def _stream(stream: Optional[torch.cuda.Stream]) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the current stream's handle without the Stream object around it (0.1 us instead of 3 us a call)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _p(t: Optional[torch.Tensor], dtype: Optional[torch.dtype] = None) -> Optional[int]:
@@ -53,32 +55,43 @@ def _ld(t: torch.Tensor) -> int:
     return t.stride(0)
 
 
-def _check(where: str, dtype: torch.dtype, *tensors: Optional[torch.Tensor]) -> None:
-    """Tensors of one type on the current device (None passes)."""
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise KalmError(1, where, "tensors must live on the CUDA device")
-        if t.dtype != dtype:
-            raise KalmError(1, where, f"expected {dtype}, got {t.dtype}")
-        if t.get_device() != torch.cuda.current_device():
-            raise KalmError(1, where, f"tensor on {t.device}, current device is cuda:{torch.cuda.current_device()}")
+def _refuse(where: str, name: str, t: torch.Tensor, dtype: torch.dtype, dev: int, what: str) -> None:
+    """Raise for a tensor that is not `what` of this type on the current device."""
+    if t.dtype is not dtype:
+        what = f"expected {dtype}, got {t.dtype}"
+    elif t.get_device() != dev:
+        what = f"tensor on {t.device}, current device is cuda:{dev}"
+    raise KalmError(1, where, f"{name}: {what}")
 
 
-def _rows(where: str, name: str, t: torch.Tensor, rows: Optional[int] = None, width: Optional[int] = None) -> int:
-    """Row stride (elements) of a 2-D view with contiguous rows, after checking its sizes."""
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1):
-        raise KalmError(1, where, f"{name}: expected a 2-D tensor with contiguous rows")
-    if (rows is not None and t.shape[0] != rows) or (width is not None and t.shape[1] != width):
-        raise KalmError(1, where, f"{name} has shape {tuple(t.shape)}, expected ({rows}, {width})")
+def _device(where: str, t: torch.Tensor) -> int:
+    """The current device, on which the call's tensors must live."""
+    if not t.is_cuda:
+        raise KalmError(1, where, "tensors must live on the CUDA device")
+    return torch.cuda.current_device()
+
+
+def _mat(where: str, name: str, t: torch.Tensor, dtype: torch.dtype, dev: int, rows: int = -1, width: int = -1) -> int:
+    """Row stride (elements) of a 2-D view with contiguous rows, after checking type, device and sizes."""
+    shape = t.shape
+    if t.dtype is not dtype or t.get_device() != dev or len(shape) != 2 or (rows >= 0 and shape[0] != rows) or \
+            (width >= 0 and shape[1] != width):
+        _refuse(where, name, t, dtype, dev, f"shape {tuple(shape)}, expected ({'rows' if rows < 0 else rows}, "
+                                            f"{'columns' if width < 0 else width})")
+    ld, step = t.stride()
+    if step != 1 and shape[1] > 1:
+        _refuse(where, name, t, dtype, dev, "expected contiguous rows")
     # the stride of a single row is arbitrary in torch; any that covers the row will do
-    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 16) * 16
+    return ld if shape[0] > 1 else -(-shape[1] // 16) * 16
 
 
-def _vector(where: str, name: str, t: Optional[torch.Tensor], n: int) -> None:
-    if t is not None and (t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1)):
-        raise KalmError(1, where, f"{name}: expected a contiguous vector of {n}")
+def _vec(where: str, name: str, t: Optional[torch.Tensor], dtype: torch.dtype, dev: int, n: int) -> Optional[int]:
+    """Address of a contiguous vector of n values (None passes)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != dev or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        _refuse(where, name, t, dtype, dev, f"shape {tuple(t.shape)}, expected a contiguous vector of {n}")
+    return t.data_ptr()
 
 
 def kalm_version() -> int:
@@ -303,24 +316,22 @@ def kalm_linear_rope(x: torch.Tensor, w: torch.Tensor, y: torch.Tensor, q_off: t
          _p(table, torch.float32), _stream(stream))
 
 
-def _cache_args(where: str, row_off: torch.Tensor, page_table: torch.Tensor, page_rows: int, codes: torch.Tensor,
-                scales: torch.Tensor, width: int, first_row: Optional[torch.Tensor] = None):
+def _cache_args(where: str, dev: int, row_off: torch.Tensor, page_table: torch.Tensor, page_rows: int,
+                codes: torch.Tensor, scales: torch.Tensor, width: int):
     """Checks what the calls on a document cache share; (n_docs, ld_table, n_pages, ld_codes, ld_scales)."""
-    _check(where, torch.int64, row_off)
-    _check(where, torch.int32, page_table, first_row)
-    _check(where, torch.uint8, codes, scales)
     n_docs = row_off.numel() - 1
     if n_docs < 0:
         raise KalmError(1, where, "the offsets are empty")
-    _vector(where, "offsets", row_off, n_docs + 1)
-    _vector(where, "first_row", first_row, n_docs)
-    if page_table.dim() != 2 or page_table.shape[0] != n_docs or not page_table.is_contiguous():
-        raise KalmError(1, where, f"page_table: expected a contiguous [{n_docs}][pages] tensor")
-    if page_rows <= 0 or codes.shape[0] % page_rows:
-        raise KalmError(1, where, f"{codes.shape[0]} cache rows are not whole pages of {page_rows}")
-    ld_codes = _rows(where, "codes", codes, None, width)
-    ld_scales = _rows(where, "scales", scales, codes.shape[0], width // CACHE_GROUP)
-    return n_docs, page_table.shape[1], codes.shape[0] // page_rows, ld_codes, ld_scales
+    _vec(where, "offsets", row_off, torch.int64, dev, n_docs + 1)
+    if page_table.dtype is not torch.int32 or page_table.get_device() != dev or page_table.dim() != 2 or \
+            page_table.shape[0] != n_docs or not page_table.is_contiguous():
+        _refuse(where, "page_table", page_table, torch.int32, dev, f"expected a contiguous [{n_docs}][pages] tensor")
+    ld_codes = _mat(where, "codes", codes, torch.uint8, dev, -1, width)
+    cached = codes.shape[0]
+    if page_rows <= 0 or cached % page_rows:
+        raise KalmError(1, where, f"{cached} cache rows are not whole pages of {page_rows}")
+    ld_scales = _mat(where, "scales", scales, torch.uint8, dev, cached, width // CACHE_GROUP)
+    return n_docs, page_table.shape[1], cached // page_rows, ld_codes, ld_scales
 
 
 def kalm_cache_write(src: torch.Tensor, row_off: torch.Tensor, page_table: torch.Tensor, page_rows: int,
@@ -333,13 +344,14 @@ def kalm_cache_write(src: torch.Tensor, row_off: torch.Tensor, page_table: torch
     [n_docs][pages]; codes uint8 [n_pages * page_rows][width]; scales uint8 [same rows][width / 32].
     No two rows may have the same place."""
     where = "kalm_cache_write"
-    _check(where, torch.bfloat16, src)
-    ld_src = _rows(where, "src", src)
-    n_docs, ld_table, n_pages, ld_codes, ld_scales = _cache_args(where, row_off, page_table, page_rows, codes, scales,
-                                                                 src.shape[1], first_row)
-    call(where, src.data_ptr(), ld_src, row_off.data_ptr(), n_docs, src.shape[0], src.shape[1],
-         None if first_row is None else first_row.data_ptr(), page_table.data_ptr(), ld_table, page_rows, n_pages,
-         codes.data_ptr(), ld_codes, scales.data_ptr(), ld_scales, _stream(stream))
+    dev = _device(where, src)
+    ld_src = _mat(where, "src", src, torch.bfloat16, dev)
+    rows, width = src.shape
+    n_docs, ld_table, n_pages, ld_codes, ld_scales = _cache_args(where, dev, row_off, page_table, page_rows, codes,
+                                                                 scales, width)
+    call(where, src.data_ptr(), ld_src, row_off.data_ptr(), n_docs, rows, width,
+         _vec(where, "first_row", first_row, torch.int32, dev, n_docs), page_table.data_ptr(), ld_table, page_rows,
+         n_pages, codes.data_ptr(), ld_codes, scales.data_ptr(), ld_scales, _stream(stream))
 
 
 def kalm_cache_read(codes: torch.Tensor, scales: torch.Tensor, row_off: torch.Tensor, page_table: torch.Tensor,
@@ -347,12 +359,13 @@ def kalm_cache_read(codes: torch.Tensor, scales: torch.Tensor, row_off: torch.Te
     """Read cached rows back into packed bf16 rows: dst[row_off[d] + i] = row first_row[d] + i of
     document d (the stored values exactly).  Arguments as kalm_cache_write."""
     where = "kalm_cache_read"
-    _check(where, torch.bfloat16, dst)
-    ld_dst = _rows(where, "dst", dst)
-    n_docs, ld_table, n_pages, ld_codes, ld_scales = _cache_args(where, row_off, page_table, page_rows, codes, scales,
-                                                                 dst.shape[1], first_row)
-    call(where, codes.data_ptr(), ld_codes, scales.data_ptr(), ld_scales, row_off.data_ptr(), n_docs, dst.shape[0],
-         dst.shape[1], None if first_row is None else first_row.data_ptr(), page_table.data_ptr(), ld_table, page_rows,
+    dev = _device(where, dst)
+    ld_dst = _mat(where, "dst", dst, torch.bfloat16, dev)
+    rows, width = dst.shape
+    n_docs, ld_table, n_pages, ld_codes, ld_scales = _cache_args(where, dev, row_off, page_table, page_rows, codes,
+                                                                 scales, width)
+    call(where, codes.data_ptr(), ld_codes, scales.data_ptr(), ld_scales, row_off.data_ptr(), n_docs, rows, width,
+         _vec(where, "first_row", first_row, torch.int32, dev, n_docs), page_table.data_ptr(), ld_table, page_rows,
          n_pages, dst.data_ptr(), ld_dst, _stream(stream))
 
 
@@ -372,47 +385,47 @@ def kalm_merged_attention_cache(q: torch.Tensor, k_self: torch.Tensor, v_self: t
     workspace: bf16 scratch [>= kalm_merged_attention_cache_rows(cached rows, n_docs)][2 * n_kv * head_dim];
     None allocates one for this call, for as many rows as the page table has places."""
     where = "kalm_merged_attention_cache"
-    if scale is None:
-        scale = head_dim ** -0.5
-    _check(where, torch.bfloat16, q, k_self, v_self, out)
-    _check(where, torch.int64, q_off, in_off)
-    _check(where, torch.int32, order)
-    _check(where, torch.float32, lse)
-    n_docs, ld_table, n_pages, ld_codes, ld_scales = _cache_args(where, pool_off, page_table, page_rows, k_codes,
-                                                                 k_scales, n_kv * head_dim)
-    _check(where, torch.uint8, v_codes, v_scales)
-    rows, cached = q.shape[0], k_codes.shape[0]
-    if _rows(where, "v_codes", v_codes, cached, n_kv * head_dim) != ld_codes or \
-            _rows(where, "v_scales", v_scales, cached, n_kv * head_dim // CACHE_GROUP) != ld_scales:
-        raise KalmError(1, where, "the cached K and V must share their row strides")
-    ld_self = _rows(where, "k_self", k_self, rows, n_kv * head_dim)
-    if _rows(where, "v_self", v_self, rows, n_kv * head_dim) != ld_self:
-        raise KalmError(1, where, "K and V views must share a row stride")
-    ldq = _rows(where, "q", q, rows, n_q * head_dim)
-    ldo = _rows(where, "out", out, None, n_q * head_dim)
-    _vector(where, "q_off", q_off, n_docs + 1)
-    _vector(where, "in_off", in_off, n_docs)
-    total_q = out.shape[0] if total_q is None else total_q
+    bf16, u8 = torch.bfloat16, torch.uint8
+    dev = _device(where, q)
+    width, rows = n_kv * head_dim, q.shape[0]
+    n_docs, ld_table, n_pages, ld_codes, ld_scales = _cache_args(where, dev, pool_off, page_table, page_rows, k_codes,
+                                                                 k_scales, width)
+    cached = n_pages * page_rows
+    ld_self = _mat(where, "k_self", k_self, bf16, dev, rows, width)
+    if _mat(where, "v_self", v_self, bf16, dev, rows, width) != ld_self or \
+            _mat(where, "v_codes", v_codes, u8, dev, cached, width) != ld_codes or \
+            _mat(where, "v_scales", v_scales, u8, dev, cached, width // CACHE_GROUP) != ld_scales:
+        raise KalmError(1, where, "K and V must share their row strides")
+    ldq = _mat(where, "q", q, bf16, dev, rows, n_q * head_dim)
+    ldo = _mat(where, "out", out, bf16, dev, -1, n_q * head_dim)
+    if total_q is None:
+        total_q = out.shape[0]
     if total_q > out.shape[0] or (in_off is None and total_q > rows):
         raise KalmError(1, where, f"total_q={total_q} exceeds the rows of out ({out.shape[0]}) or q ({rows})")
-    if lse is not None and (not lse.is_contiguous() or lse.dim() != 2 or lse.shape[0] < total_q or lse.shape[1] != n_q):
-        raise KalmError(1, where, f"lse: expected a contiguous [{total_q}][{n_q}] tensor")
-    if order is not None and order.numel() < kalm_attention_items(n_docs, max_q, n_q, n_kv, last_tile_only):
-        raise KalmError(1, where, "order is shorter than the call's work items")
+    if lse is not None and (lse.dtype is not torch.float32 or lse.get_device() != dev or lse.dim() != 2 or
+                            lse.shape[0] < total_q or lse.shape[1] != n_q or not lse.is_contiguous()):
+        _refuse(where, "lse", lse, torch.float32, dev, f"expected a contiguous [{total_q}][{n_q}] tensor")
+    if order is not None:
+        items = kalm_attention_items(n_docs, max_q, n_q, n_kv, last_tile_only)
+        if order.dtype is not torch.int32 or order.get_device() != dev or order.numel() < items or \
+                not order.is_contiguous():
+            _refuse(where, "order", order, torch.int32, dev, f"expected at least the call's {items} work items")
     if workspace is None:
-        with torch.cuda.stream(stream):  # the allocator hands memory out per stream
-            workspace = torch.empty(n_docs * (ld_table * page_rows + 64), 2 * n_kv * head_dim, dtype=torch.bfloat16,
-                                    device=q.device)
-    else:
-        _check(where, torch.bfloat16, workspace)
-        if workspace.dim() != 2 or not workspace.is_contiguous() or workspace.shape[1] != 2 * n_kv * head_dim:
-            raise KalmError(1, where, f"workspace: expected a contiguous [rows][{2 * n_kv * head_dim}] tensor")
+        shape = (n_docs * (ld_table * page_rows + 64), 2 * width)  # every place of the table, see the rows helper below
+        if stream is None:
+            workspace = torch.empty(shape, dtype=bf16, device=q.device)
+        else:
+            with torch.cuda.stream(stream):  # the allocator hands memory out per stream
+                workspace = torch.empty(shape, dtype=bf16, device=q.device)
+    elif _mat(where, "workspace", workspace, bf16, dev, -1, 2 * width) != 2 * width:
+        raise KalmError(1, where, "the workspace must be contiguous")
     call(where, q.data_ptr(), ldq, k_self.data_ptr(), v_self.data_ptr(), ld_self, k_codes.data_ptr(),
          v_codes.data_ptr(), ld_codes, k_scales.data_ptr(), v_scales.data_ptr(), ld_scales, page_table.data_ptr(),
-         ld_table, page_rows, n_pages, q_off.data_ptr(), None if in_off is None else in_off.data_ptr(), rows,
-         pool_off.data_ptr(), n_docs, int(max_q), int(total_q), n_q, n_kv, head_dim, float(scale),
-         1 if last_tile_only else 0, None if order is None else order.data_ptr(), workspace.data_ptr(),
-         workspace.shape[0], out.data_ptr(), ldo, None if lse is None else lse.data_ptr(), _stream(stream))
+         ld_table, page_rows, n_pages, _vec(where, "q_off", q_off, torch.int64, dev, n_docs + 1),
+         _vec(where, "in_off", in_off, torch.int64, dev, n_docs), rows, pool_off.data_ptr(), n_docs, max_q, total_q,
+         n_q, n_kv, head_dim, head_dim ** -0.5 if scale is None else scale, 1 if last_tile_only else 0,
+         None if order is None else order.data_ptr(), workspace.data_ptr(), workspace.shape[0], out.data_ptr(), ldo,
+         None if lse is None else lse.data_ptr(), _stream(stream))
 
 
 def kalm_merged_attention_cache_rows(total_pool: int, n_docs: int) -> int:
@@ -424,11 +437,11 @@ def kalm_rms_norm(x: torch.Tensor, w: torch.Tensor, h: torch.Tensor, eps: float 
                   stream=None) -> None:
     """h = x / sqrt(mean(x^2) + eps) * (w + weight_offset), row by row; h may be x."""
     where = "kalm_rms_norm"
-    _check(where, torch.bfloat16, x, w, h)
+    dev = _device(where, x)
+    ldx = _mat(where, "x", x, torch.bfloat16, dev)
     rows, width = x.shape
-    _vector(where, "w", w, width)
-    call(where, x.data_ptr(), _rows(where, "x", x), w.data_ptr(), h.data_ptr(), _rows(where, "h", h, rows, width), rows,
-         width, eps, weight_offset, _stream(stream))
+    call(where, x.data_ptr(), ldx, _vec(where, "w", w, torch.bfloat16, dev, width), h.data_ptr(),
+         _mat(where, "h", h, torch.bfloat16, dev, rows, width), rows, width, eps, weight_offset, _stream(stream))
 
 
 def kalm_norm_residual(y: torch.Tensor, x: torch.Tensor, x_out: torch.Tensor, h: Optional[torch.Tensor] = None,
@@ -442,29 +455,26 @@ def kalm_norm_residual(y: torch.Tensor, x: torch.Tensor, x_out: torch.Tensor, h:
     row offsets).  With q_off only the documents' rows are computed.  w_post None: y enters without a
     norm; h and w_pre go together.  x_out may be x."""
     where = "kalm_norm_residual"
-    _check(where, torch.bfloat16, y, x, x_out, h, w_post, w_pre, gate)
-    _check(where, torch.int64, q_off)
+    bf16 = torch.bfloat16
+    dev = _device(where, x)
+    ldx = _mat(where, "x", x, bf16, dev)
     rows, width = x.shape
-    _vector(where, "w_post", w_post, width)
-    _vector(where, "w_pre", w_pre, width)
     n_docs = 0 if q_off is None else q_off.numel() - 1
     if n_docs < 0:
         raise KalmError(1, where, "the offsets are empty")
-    if q_off is not None:
-        _vector(where, "q_off", q_off, n_docs + 1)
-    ld_gate = 0
-    if gate is not None:
-        if gate.dim() == 2:
-            if q_off is None:
-                raise KalmError(1, where, "a gate per document needs q_off")
-            ld_gate = _rows(where, "gate", gate, n_docs, width)
-        else:
-            _vector(where, "gate", gate, width)
-    p = lambda t: None if t is None else t.data_ptr()
-    call(where, y.data_ptr(), _rows(where, "y", y, rows, width), x.data_ptr(), _rows(where, "x", x), p(w_post), p(gate),
-         ld_gate, p(q_off), n_docs, residual_scale, x_out.data_ptr(), _rows(where, "x_out", x_out, rows, width),
-         p(w_pre), p(h), 0 if h is None else _rows(where, "h", h, rows, width), rows, width, eps, weight_offset,
-         _stream(stream))
+    ld_gate, gate_at = 0, None
+    if gate is not None and gate.dim() == 2:
+        if q_off is None:
+            raise KalmError(1, where, "a gate per document needs q_off")
+        ld_gate, gate_at = _mat(where, "gate", gate, bf16, dev, n_docs, width), gate.data_ptr()
+    else:
+        gate_at = _vec(where, "gate", gate, bf16, dev, width)
+    call(where, y.data_ptr(), _mat(where, "y", y, bf16, dev, rows, width), x.data_ptr(), ldx,
+         _vec(where, "w_post", w_post, bf16, dev, width), gate_at, ld_gate,
+         _vec(where, "q_off", q_off, torch.int64, dev, n_docs + 1), n_docs, residual_scale, x_out.data_ptr(),
+         _mat(where, "x_out", x_out, bf16, dev, rows, width), _vec(where, "w_pre", w_pre, bf16, dev, width),
+         None if h is None else h.data_ptr(), 0 if h is None else _mat(where, "h", h, bf16, dev, rows, width), rows,
+         width, eps, weight_offset, _stream(stream))
 
 
 def kalm_selftest_wait_timeout(wait_ns: int, stream=None) -> None:

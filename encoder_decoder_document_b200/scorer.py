@@ -9,6 +9,13 @@ buffers, and runs, on one stream:
   kalm_merged_attention, kalm_linear (output projection + residual) ->
   kalm_yes_no_score.
 
+With norm weights (``DeviceWeights.w_norm_pre`` and the fields after it) every
+block reads kalm_rms_norm / kalm_norm_residual outputs instead of the plain
+residual stream.  Documents that many queries name can live in a
+``DocumentCache`` (``new_cache``, ``cache_put``): ``rerank_cached`` scores any of
+them, the attention reading their cross K/V in 8 bits
+(kalm_merged_attention_cache).
+
 Python only sequences the calls and owns the buffers; every step runs in the
 CUDA kernels of libkalm.  ``capture()`` records the whole sequence in a CUDA
 graph so a query costs one graph launch.  ``rerank()`` is the user-facing call:
@@ -28,7 +35,9 @@ from . import (kalm_broadcast_rows, kalm_check_device_errors, kalm_chunk_pool, k
                kalm_device_check, kalm_linear, kalm_merged_attention_out_proj, kalm_attention_out_proj_sync_len,
                kalm_merged_attention, kalm_ragged_offsets, kalm_yes_no_score, kalm_attention_items,
                kalm_attention_schedule, kalm_linear_rope, kalm_rope_table, kalm_linear_chain,
-               kalm_linear_chain_rope, kalm_linear_chain_sync_len)
+               kalm_linear_chain_rope, kalm_linear_chain_sync_len, kalm_merged_attention_cache,
+               kalm_merged_attention_cache_rows, kalm_norm_residual, kalm_rms_norm)
+from .document_cache import CacheView, DocumentCache
 
 HEAD_DIM = 256
 # the pages' runtime limits ("Runtime boundaries"): passages of at most 1,024 encoder
@@ -50,6 +59,14 @@ class DeviceWeights:
     w_kv_cross: torch.Tensor  # [L][2 n_kv D][H]
     w_yes: torch.Tensor       # [H]
     w_no: torch.Tensor        # [H]
+    # the norms around the blocks (None: the plain residual stack)
+    w_norm_pre: Optional[torch.Tensor] = None    # [L][H], before each block's Q|K|V projection
+    w_norm_post: Optional[torch.Tensor] = None   # [L][H], of each block's output
+    gate: Optional[torch.Tensor] = None          # [L][H], times the (normed) block output
+    w_norm_final: Optional[torch.Tensor] = None  # [H], before the readout
+    norm_eps: float = 1e-6
+    norm_weight_offset: float = 0.0              # 1.0 for checkpoints that store the weights minus one
+    residual_scale: float = 1.0                  # of the residual stream at each block's sum
 
     @classmethod
     def from_bits(cls, w, device="cuda") -> "DeviceWeights":
@@ -76,6 +93,12 @@ class FBNLScorer:
         assert qkv_rows == (n_q + 2 * n_kv) * head_dim
         self.scale = head_dim ** -0.5
         self.prune = prune
+        self.norms = weights.w_norm_pre is not None
+        if not self.norms and (weights.w_norm_post is not None or weights.gate is not None or
+                               weights.w_norm_final is not None or weights.residual_scale != 1.0):
+            raise ValueError("w_norm_post, gate, w_norm_final and residual_scale need w_norm_pre")
+        if self.norms and fused_out:
+            raise ValueError("fused_out adds the residual in its projection: it does not go with norms")
         self.rope_theta = rope_theta  # rotary base for the decoder's self Q/K, or None (no rotation)
         # attention and output projection of every layer but the pruned last one in one
         # launch (kalm_merged_attention_out_proj)
@@ -83,7 +106,8 @@ class FBNLScorer:
         # each layer's output projection and the next layer's Q|K|V projection in one launch
         # (kalm_linear_chain, or kalm_linear_chain_rope with rotation), in the pruned stack
         # without the fused layer
-        self.chain = chain and prune and not fused_out
+        self.chain = chain and prune and not fused_out and not self.norms
+        self.view: Optional[CacheView] = None  # documents of a DocumentCache being scored
         self._qkv_ready = -1  # layer whose Q|K|V the last chained launch produced
         # the rotary angles' (cos, sin), built once for this base
         self.rope_tab = kalm_rope_table(rope_theta, head_dim) if rope_theta is not None else None
@@ -126,6 +150,9 @@ class FBNLScorer:
         self.qkv = torch.empty(rows, (self.n_q + 2 * self.n_kv) * D, dtype=torch.bfloat16, **kw)
         self.o = torch.empty(rows, self.n_q * D, dtype=torch.bfloat16, **kw)
         self.x = torch.empty(rows, H, dtype=torch.bfloat16, **kw)
+        if self.norms:  # a block's normed input (and that of the query's common rows), and its output
+            self.h, self.y = (torch.empty(rows, H, dtype=torch.bfloat16, **kw) for _ in range(2))
+            self.h0 = torch.empty(lq, H, dtype=torch.bfloat16, **kw)
         # (yes, no, margin, score) rows of one buffer: one device->host copy per query
         self.result = torch.empty(4, n_docs, dtype=torch.float32, **kw)
         # work order of the full-layer attention launches (same costs in every layer)
@@ -156,6 +183,7 @@ class FBNLScorer:
         """Offsets, attention work order, pooled document cache.  With a ``side`` stream
         the work order and the query input broadcast (both need only the offsets) run
         there, beside the pooling and the cross projection; the caller joins it."""
+        self.view = None  # the documents are this query's own
         kalm_ragged_offsets(self.doc_len, self.tok_off, self.pool_off, self.chunk)
         self._mark("offsets")
         if side is not None:
@@ -196,14 +224,30 @@ class FBNLScorer:
         self._mark("qkv_proj")
 
     def layer_qkv(self, l: int) -> None:
-        self.qkv_proj(self.x, l, self.qkv, self.q_off)
+        self.qkv_proj(self.h if self.norms else self.x, l, self.qkv, self.q_off)
+
+    def attend(self, l: int, q, ks, vs, in_off=None, last_tile_only: bool = False) -> None:
+        """Merged attention of layer l into self.o, over this query's own documents or the cached ones."""
+        if self.view is None:
+            kc, vc = self.cross_views(l)
+            kalm_merged_attention(q, ks, vs, kc, vc, self.q_off, self.pool_off, self.lq, self.n_q, self.n_kv, self.o,
+                                  self.scale, in_off=in_off, last_tile_only=last_tile_only,
+                                  order=None if last_tile_only else self.order)
+        else:
+            cache, w = self.view_cache, self.n_kv * self.D
+            k, v = 2 * l * w, (2 * l + 1) * w
+            g = cache.width // cache.scales.shape[1]
+            kalm_merged_attention_cache(q, ks, vs, cache.codes[:, k:k + w], cache.scales[:, k // g:(k + w) // g],
+                                        cache.codes[:, v:v + w], cache.scales[:, v // g:(v + w) // g],
+                                        self.view.page_table, cache.page_rows, self.q_off, self.view.row_off, self.lq,
+                                        self.n_q, self.n_kv, self.o, self.scale, in_off=in_off,
+                                        last_tile_only=last_tile_only,
+                                        order=None if last_tile_only else self.view_order, workspace=self.view_ws)
+        self._mark("merged_attention")
 
     def layer_attention(self, l: int) -> None:
         q, ks, vs = self.qkv_views()
-        kc, vc = self.cross_views(l)
-        kalm_merged_attention(q, ks, vs, kc, vc, self.q_off, self.pool_off, self.lq, self.n_q, self.n_kv, self.o,
-                              self.scale, order=self.order)
-        self._mark("merged_attention")
+        self.attend(l, q, ks, vs)
 
     def _join_side(self) -> None:
         """The residual stream X is first read by an output projection: wait for the
@@ -217,6 +261,30 @@ class FBNLScorer:
         kalm_linear(self.o, self.w.w_o[l], self.x, residual=self.x)
         self._mark("o_proj")
 
+    def block_out(self, l: int, last_rows_only: bool = False) -> None:
+        """With norms: output projection of block l, its norm and gate, the residual sum and the norm
+        before what comes next (block l + 1, or the readout), of every row or each document's last."""
+        rows = slice(self.lq - 1, None, self.lq) if last_rows_only else slice(None)
+        o, y, x, h = self.o[rows], self.y[rows], self.x[rows], self.h[rows]
+        w = self.w
+        self._join_side()
+        kalm_linear(o, w.w_o[l], y)
+        self._mark("o_proj")
+        w_next = w.w_norm_pre[l + 1] if l + 1 < self.L else w.w_norm_final
+        kalm_norm_residual(y, x, x, h=h if w_next is not None else None,
+                           w_post=w.w_norm_post[l] if w.w_norm_post is not None else None, w_pre=w_next,
+                           gate=w.gate[l] if w.gate is not None else None, residual_scale=w.residual_scale,
+                           eps=w.norm_eps, weight_offset=w.norm_weight_offset)
+        self._mark("norm_residual")
+
+    def first_norm(self, x: torch.Tensor, h: torch.Tensor) -> torch.Tensor:
+        """Block 0's input: the norm of x into h, or x itself without norms."""
+        if not self.norms:
+            return x
+        kalm_rms_norm(x, self.w.w_norm_pre[0], h, eps=self.w.norm_eps, weight_offset=self.w.norm_weight_offset)
+        self._mark("rms_norm")
+        return h
+
     def attention_out(self, l: int, q, ks, vs, in_off=None) -> None:
         """Fused attention + output projection of layer l (X updated in place)."""
         kc, vc = self.cross_views(l)
@@ -227,22 +295,27 @@ class FBNLScorer:
         self._mark("attention_out_proj")
 
     def layer(self, l: int) -> None:
+        if l == 0:
+            self.first_norm(self.x, self.h if self.norms else self.x)
         self.layer_qkv(l)
-        if self.fused_out:
+        if self.fused_out and self.view is None:
             q, ks, vs = self.qkv_views()
             self.attention_out(l, q, ks, vs)
             return
         self.layer_attention(l)
-        self.layer_out(l)
+        if self.norms:
+            self.block_out(l)
+        else:
+            self.layer_out(l)
 
     def layer_pruned(self, l: int) -> None:
         """Layer l with the exact pruning described in the class docstring."""
         first, last = l == 0, l == self.L - 1
         Lq = self.lq
-        kc, vc = self.cross_views(l)
         if first:
             # every document's decoder input is the query's common input: one Q|K|V for all
-            self.qkv_proj(self.x0, l, self.qkv[:Lq], self.one_doc_off)
+            self.qkv_proj(self.first_norm(self.x0, self.h0 if self.norms else self.x0), l, self.qkv[:Lq],
+                          self.one_doc_off)
             q, ks, vs = (t[:Lq] for t in self.qkv_views())
             in_off = self.zero_off
         else:
@@ -250,13 +323,13 @@ class FBNLScorer:
                 self.layer_qkv(l)
             q, ks, vs = self.qkv_views()
             in_off = None
-        if self.fused_out and not last:
+        if self.fused_out and not last and self.view is None:
             self.attention_out(l, q, ks, vs, in_off)
             return
-        kalm_merged_attention(q, ks, vs, kc, vc, self.q_off, self.pool_off, Lq, self.n_q, self.n_kv, self.o,
-                              self.scale, in_off=in_off, last_tile_only=last, order=None if last else self.order)
-        self._mark("merged_attention")
-        if last:
+        self.attend(l, q, ks, vs, in_off, last)
+        if self.norms:
+            self.block_out(l, last_rows_only=last)
+        elif last:
             # only each document's final row reaches the readout
             x_last = self.x[Lq - 1::Lq]
             self._join_side()
@@ -276,7 +349,8 @@ class FBNLScorer:
             self.layer_out(l)
 
     def readout(self) -> None:
-        kalm_yes_no_score(self.x, self.q_off, self.w.w_yes, self.w.w_no, self.yes, self.no, self.score,
+        hidden = self.h if self.w.w_norm_final is not None else self.x
+        kalm_yes_no_score(hidden, self.q_off, self.w.w_yes, self.w.w_no, self.yes, self.no, self.score,
                           self.margin)
         self._mark("yes_no_score")
 
@@ -539,6 +613,76 @@ class FBNLScorer:
         # device: raise instead of returning scores computed past it
         self.check_errors()
         return np.ascontiguousarray(res.T)
+
+    # ------------------------------------------------------------------ 8-bit document cache
+    def new_cache(self, n_pages: int, page_rows: int = 64, device="cuda") -> DocumentCache:
+        """A cache for this stack: a row holds the cross K/V of every layer of one pooled vector
+        (kalm_cross_kv_proj's layout) in 8 bits, n_layers * 2 * n_kv * head_dim * 33 / 32 bytes."""
+        return DocumentCache(n_pages, self.L * 2 * self.n_kv * self.D, page_rows, device)
+
+    def cache_put(self, cache: DocumentCache, keys, enc: np.ndarray, doc_len: np.ndarray) -> None:
+        """Pool documents, project their cross K/V and store them under ``keys``; arguments as for
+        ``rerank`` (enc: bf16 bits of the documents' encoder states, packed)."""
+        self._check_cache(cache)
+        doc_len = np.asarray(doc_len)
+        if doc_len.ndim != 1 or len(keys) != doc_len.shape[0]:
+            raise ValueError("cache_put: doc_len must be one length per document")
+        if doc_len.size and (doc_len.min() < 0 or doc_len.max() > MAX_DOC_TOKENS):
+            raise ValueError(f"cache_put: document lengths must lie in [0, {MAX_DOC_TOKENS}]")
+        doc_len = doc_len.astype(np.int32)
+        n, tokens = int(doc_len.shape[0]), int(doc_len.sum())
+        if np.asarray(enc).shape[0] < tokens:
+            raise ValueError(f"cache_put: enc holds {np.asarray(enc).shape[0]} rows, doc_len sums to {tokens}")
+        rows = ((doc_len.astype(np.int64) + self.chunk - 1) // self.chunk).tolist()
+        dev = cache.device
+        kv = torch.empty(sum(rows), cache.width, dtype=torch.bfloat16, device=dev)
+        if sum(rows):
+            states = bf16_from_bits(np.asarray(enc)[:tokens], dev)
+            lens = torch.from_numpy(doc_len).to(dev)
+            tok_off, pool_off = (torch.empty(n + 1, dtype=torch.int64, device=dev) for _ in range(2))
+            pooled = torch.empty(sum(rows), self.H, dtype=torch.bfloat16, device=dev)
+            kalm_ragged_offsets(lens, tok_off, pool_off, self.chunk)
+            kalm_chunk_pool(states, tok_off, lens, pooled, pool_off, sum(rows), self.chunk)
+            kalm_cross_kv_proj(pooled, self.w.w_kv_cross, kv, self.n_kv, self.D)
+        cache.put(keys, rows, kv)
+
+    def score_rows_cached(self, x0: np.ndarray, cache: DocumentCache, keys) -> np.ndarray:
+        """Rows (yes, no, margin, score) of cached documents for one query (``[len(keys)][4]`` float32 on
+        the host), in the order of ``keys``; x0: bf16 bits [lq][H]."""
+        self._check_cache(cache)
+        lq = int(np.asarray(x0).shape[0])
+        if not 1 <= lq <= MAX_QUERY_TOKENS:
+            raise ValueError(f"rerank_cached: the query input must have 1..{MAX_QUERY_TOKENS} rows (got {lq})")
+        if len(keys) == 0:
+            return np.zeros((0, 4), dtype=np.float32)
+        view = cache.view(keys)
+        self.prepare(len(keys), 0, 0, lq)
+        self.x0.copy_(bf16_from_bits(np.asarray(x0), cache.device))
+        items = kalm_attention_items(len(keys), lq, self.n_q, self.n_kv)
+        self.view_order = torch.empty(items, dtype=torch.int32, device=cache.device)
+        kalm_attention_schedule(self.q_off, view.row_off, lq, self.n_q, self.n_kv, self.view_order)
+        # one layer's cross K/V of these documents, widened; every layer uses the same scratch
+        self.view_ws = torch.empty(kalm_merged_attention_cache_rows(view.total_rows, len(keys)), 2 * self.n_kv * self.D,
+                                   dtype=torch.bfloat16, device=cache.device)
+        self.view_cache, self.view = cache, view
+        try:
+            self.launches = 0
+            self.decode()
+            res = self.scores_to_host().numpy()
+            self.check_errors()
+        finally:
+            self.view = self.view_cache = self.view_ws = self.view_order = None
+        return np.ascontiguousarray(res.T)
+
+    def rerank_cached(self, x0: np.ndarray, cache: DocumentCache, keys, top_n: Optional[int] = None):
+        """``rerank`` over documents of a cache: [{index, relevance_score}] best first, index into ``keys``."""
+        res = self.score_rows_cached(x0, cache, keys)
+        return rank(res[:, 2], res[:, 3], top_n)
+
+    def _check_cache(self, cache: DocumentCache) -> None:
+        width = self.L * 2 * self.n_kv * self.D
+        if cache.width != width:
+            raise ValueError(f"the cache's rows have {cache.width} values, this stack's cross K/V {width}")
 
     def check_errors(self) -> None:
         """Wait for this scorer's streams and raise ``KalmError`` if a kernel recorded a
