@@ -8,9 +8,13 @@
 // Everything is held in fp32 from the loads to one rounding per output: h is the norm of t itself, not of the
 // rounded x_out.
 //
-// Bound by memory (8 bytes a value: y, x, x_out, h).  A row lives in the registers of one warp (up to 1,024
-// columns) or one block, so each input is read once; the two sums of squares are shuffles (and one exchange
-// through shared memory per sum in the block form).
+// Bound by memory (8 bytes a value: y, x, x_out, h).  A row lives in the registers of 8 lanes, a warp or a block,
+// so each input is read once; the two sums of squares are shuffles (and one exchange through shared memory
+// per sum in the block form).  Pairs of values share an instruction (f32x2), which halved the issue slots
+// (121 -> 108 us at 26,077 x 2,560); a document's gate is asked for before the first sum, not after it (108 -> 90
+// us: it comes from L2, and its latency stood behind the sum's).
+// Measured (CUDA graph of calls over three sets of inputs): 12,800 x 640 15 us = 4.4 TB/s; 25,600 x 1,152 45 us =
+// 5.2 TB/s; 26,077 x 2,560 90 us = 5.9 TB/s (0.91 of the copy bandwidth).
 #include <cmath>
 
 #include "kalm.h"
@@ -22,6 +26,7 @@ namespace {
 
 constexpr int kWarpRowThreads = 256;  // block of the warp-per-row form
 constexpr int kMaxWidth = KALM_NORM_MAX_WIDTH;
+constexpr int kMaxSpan = (kMaxWidth / 8 + 159) / 160 * 32;  // threads of the widest row: five 8-column units each
 
 struct NormParams {
   const uint4* y;       // block output, or NULL: a norm of x alone
@@ -39,26 +44,50 @@ struct NormParams {
   float residual_scale, weight_offset, eps, inv_width;
 };
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    f[2 * k] = __uint_as_float(w[k] << 16);
-    f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-  }
+// Two fp32 values in a register pair; the SM works on both with one instruction.
+using F2 = uint64_t;
+__device__ __forceinline__ F2 pair2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 unpack2(uint32_t w) {  // a bf16 pair, exact
+  return pair2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float2 split2(F2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack2(F2 v) {
+  const float2 f = split2(v);
+  return pack_bf16x2(f.x, f.y);
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
-}
-
-// Sum over the row's threads: the warp, or the block (through `part`, one slot per warp).
-template <bool BLOCK>
-__device__ __forceinline__ float row_sum(float v, float* part) {
+// A row's sum over its SPAN threads: SPAN lanes of a warp (a power of two), or the whole block where SPAN
+// is 0 (through `part`, one slot per warp).
+template <int SPAN>
+__device__ __forceinline__ float row_sum(F2 v2, float* part) {
+  const float2 f = split2(v2);
+  float v = f.x + f.y;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (BLOCK) {
+  for (int o = (SPAN ? SPAN : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (!SPAN) {
     const int warps = blockDim.x >> 5;
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
@@ -69,127 +98,155 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
 }
 
 // V: 8-column units a thread holds; unit i of thread t is i * (threads of the row) + t.
-template <int V, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? kMaxWidth / 32 : kWarpRowThreads) norm_kernel(const NormParams p) {
+template <int V, int SPAN>
+__global__ void __launch_bounds__(SPAN ? kWarpRowThreads : kMaxSpan) norm_kernel(const NormParams p) {
   pdl_launch_dependents();
   pdl_wait_predecessor();
-  __shared__ float part[2][kMaxWidth / 1024];
+  __shared__ float part[2][kMaxSpan / 32];
   const int lane = threadIdx.x & 31;
-  const int span = BLOCK ? blockDim.x : 32;
-  const int t = BLOCK ? threadIdx.x : lane;
-  const int64_t row = BLOCK ? static_cast<int64_t>(blockIdx.x)
-                            : static_cast<int64_t>(blockIdx.x) * (kWarpRowThreads / 32) + (threadIdx.x >> 5);
-  if (row >= p.rows) return;
+  const int span = SPAN ? SPAN : blockDim.x;
+  const int t = SPAN ? lane & (SPAN - 1) : threadIdx.x;
+  const int64_t row = SPAN ? (static_cast<int64_t>(blockIdx.x) * kWarpRowThreads + threadIdx.x) / (SPAN ? SPAN : 1)
+                           : static_cast<int64_t>(blockIdx.x);
+  // rows of no document, or past the last, are computed as zeros (their threads take part in the shuffles) and not written
+  bool there = row < p.rows;
+  // The row's document: up to 32 threads search together, four offsets each a round.  The first round's
+  // offsets are asked for before x and y: loads come back in order, so that up to 128 documents cost the
+  // latency of no load but the gate's own.
+  constexpr int kWays = SPAN ? SPAN : 32;
+  const int way = lane & (kWays - 1);
+  int lo = 0, hi = p.q_off ? p.n_docs : 0, step = max(1, (hi + 4 * kWays - 1) / (4 * kWays));
+  int64_t o[4], o_first = 0, o_last = 0;
+  if (p.q_off) {
+    o_first = __ldg(p.q_off);
+    o_last = __ldg(p.q_off + p.n_docs);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int at = step * (j * kWays + way + 1);
+      o[j] = at < hi ? __ldg(p.q_off + at) : INT64_MAX;
+    }
+  }
   uint4 xv[V], yv[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = i * span + t;
     xv[i] = yv[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (c < p.nv) {
+    if (there && c < p.nv) {
       xv[i] = p.x[row * p.ldx + c];
       if (p.y) yv[i] = p.y[row * p.ldy + c];
     }
   }
-  int doc = 0;
-  if (p.q_off) {  // the row's document; a row of none is left as it was
-    int lo = 0, hi = p.n_docs;
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) / 32;
-      const int at = lo + step * (lane + 1);
-      const int n = __popc(__ballot_sync(0xffffffffu, at < hi && __ldg(p.q_off + at) <= row));
+  if (p.q_off) {
+    there = there && row >= o_first && row < o_last;
+    while (true) {
+      int n = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const unsigned below = __ballot_sync(0xffffffffu, o[j] <= row);
+        n += __popc(kWays == 32 ? below : (below >> (lane & ~(kWays - 1))) & ((1u << (kWays & 31)) - 1u));
+      }
       hi = min(hi, lo + step * (n + 1));
       lo += step * n;
-    }
-    doc = lo;
-    if (row < __ldg(p.q_off + doc) || row >= __ldg(p.q_off + doc + 1)) return;  // same for the whole row
-  }
-  float r[V][8];
-  if (p.y) {
-    float ss = 0.f;
-    if (p.w_post) {
+      if (!__any_sync(0xffffffffu, hi - lo > 1)) break;
+      step = max(1, (hi - lo + 4 * kWays - 1) / (4 * kWays));
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float f[8];
-        unpack8(yv[i], f);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) ss = fmaf(f[k], f[k], ss);
+      for (int j = 0; j < 4; ++j) {
+        const int at = lo + step * (j * kWays + way + 1);
+        o[j] = at < hi ? __ldg(p.q_off + at) : INT64_MAX;
       }
-      ss = row_sum<BLOCK>(ss, part[0]);
     }
-    const float rs = p.w_post ? rsqrtf(fmaf(ss, p.inv_width, p.eps)) : 1.f;
+    if (!SPAN && !there) return;  // the whole block's row
+  }
+  const int doc = lo;
+  const F2 off = pair2(p.weight_offset, p.weight_offset);
+  F2 r[V][4];
+  if (p.y) {
+    uint4 gv[V];  // asked for before the first sum: a document's gate comes from L2
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = i * span + t;
-      float x[8], y[8];
-      unpack8(xv[i], x);
-      unpack8(yv[i], y);
-      if (p.w_post) {
-        float w[8];
-        unpack8(c < p.nv ? __ldg(p.w_post + c) : make_uint4(0u, 0u, 0u, 0u), w);
+      gv[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.gate) gv[i] = __ldg(p.gate + doc * p.ld_gate + min(i * span + t, p.nv - 1));
+    }
+    float rs = 1.f;
+    if (p.w_post) {
+      F2 ss = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = y[k] * rs * (w[k] + p.weight_offset);
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const F2 y = unpack2((&yv[i].x)[k]);
+          ss = fma2(y, y, ss);
+        }
+      rs = rsqrtf(fmaf(row_sum<SPAN>(ss, part[0]), p.inv_width, p.eps));
+    }
+    const F2 rs2 = pair2(rs, rs), scale2 = pair2(p.residual_scale, p.residual_scale);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = min(i * span + t, p.nv - 1);  // (columns past the row are zeros, whatever their weight)
+      uint4 wv = make_uint4(0u, 0u, 0u, 0u);
+      if (p.w_post) wv = __ldg(p.w_post + c);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        F2 u = unpack2((&yv[i].x)[k]);
+        if (p.w_post) u = mul2(mul2(u, rs2), add2(unpack2((&wv.x)[k]), off));
+        const F2 x = unpack2((&xv[i].x)[k]);
+        r[i][k] = p.gate ? fma2(u, unpack2((&gv[i].x)[k]), mul2(x, scale2)) : fma2(x, scale2, u);
       }
-      if (p.gate) {
-        float g[8];
-        unpack8(c < p.nv ? __ldg(p.gate + doc * p.ld_gate + c) : make_uint4(0u, 0u, 0u, 0u), g);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] *= g[k];
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) r[i][k] = fmaf(p.residual_scale, x[k], y[k]);
-      if (p.x_out && c < p.nv) xv[i] = pack8(r[i]);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) unpack8(xv[i], r[i]);
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) r[i][k] = unpack2((&xv[i].x)[k]);
   }
+  float rs = 0.f;
   if (p.h) {
-    float ss = 0.f;
+    F2 ss = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) ss = fmaf(r[i][k], r[i][k], ss);
-    ss = row_sum<BLOCK>(ss, part[1]);
-    const float rs = rsqrtf(fmaf(ss, p.inv_width, p.eps));
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = i * span + t;
-      if (c >= p.nv) continue;
-      float w[8];
-      unpack8(__ldg(p.w_pre + c), w);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) w[k] = r[i][k] * rs * (w[k] + p.weight_offset);
-      p.h[row * p.ldh + c] = pack8(w);
-    }
+      for (int k = 0; k < 4; ++k) ss = fma2(r[i][k], r[i][k], ss);
+    rs = rsqrtf(fmaf(row_sum<SPAN>(ss, part[1]), p.inv_width, p.eps));
   }
-  if (p.x_out) {
+  const F2 rs2 = pair2(rs, rs);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = i * span + t;
-      if (c < p.nv) p.x_out[row * p.ldxo + c] = xv[i];
+  for (int i = 0; i < V; ++i) {
+    const int c = i * span + t;
+    if (!there || c >= p.nv) continue;
+    if (p.x_out)
+      p.x_out[row * p.ldxo + c] = make_uint4(pack2(r[i][0]), pack2(r[i][1]), pack2(r[i][2]), pack2(r[i][3]));
+    if (p.h) {
+      const uint4 wv = __ldg(p.w_pre + c);
+      uint32_t o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = pack2(mul2(mul2(r[i][k], rs2), add2(unpack2((&wv.x)[k]), off)));
+      p.h[row * p.ldh + c] = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
 
-template <bool BLOCK>
+template <int SPAN>
 cudaError_t launch_norm(int v, dim3 grid, dim3 block, cudaStream_t s, const NormParams& p) {
   switch (v) {
-    case 1: return launch_pdl(norm_kernel<1, BLOCK>, grid, block, 0, s, p);
-    case 2: return launch_pdl(norm_kernel<2, BLOCK>, grid, block, 0, s, p);
-    case 3: return launch_pdl(norm_kernel<3, BLOCK>, grid, block, 0, s, p);
-    default: return launch_pdl(norm_kernel<4, BLOCK>, grid, block, 0, s, p);
+    case 1: return launch_pdl(norm_kernel<1, SPAN>, grid, block, 0, s, p);
+    case 2: return launch_pdl(norm_kernel<2, SPAN>, grid, block, 0, s, p);
+    case 3: return launch_pdl(norm_kernel<3, SPAN>, grid, block, 0, s, p);
+    case 4: return launch_pdl(norm_kernel<4, SPAN>, grid, block, 0, s, p);
+    default: return launch_pdl(norm_kernel<5, SPAN>, grid, block, 0, s, p);
   }
 }
 
 kalm_status run_norm(const char* what, const NormParams& p, cudaStream_t s) {
-  cudaError_t e;
-  if (p.nv <= 128) {  // a warp per row
-    const int64_t blocks = (p.rows + kWarpRowThreads / 32 - 1) / (kWarpRowThreads / 32);
-    e = launch_norm<false>((p.nv + 31) / 32, dim3(static_cast<unsigned>(blocks)), dim3(kWarpRowThreads), s, p);
-  } else {  // a block per row, four units a thread
-    const int threads = 32 * ((p.nv + 127) / 128);
-    e = launch_norm<true>(4, dim3(static_cast<unsigned>(p.rows)), dim3(threads), s, p);
-  }
+  // The fewest threads a row with at most five units each: 8 lanes, a warp, or whole warps (a block per row).  At
+  // 26,077 x 2,560 (a gate per document) 64 threads x 5 units took 90 us, 96 x 4 100, 128 x 3 98, 160 x 2 100; at
+  // 25,600 x 1,152 32 x 5 took 45 us, 64 x 3 47, 96 x 2 52; at 12,800 x 640 32 x 3 took 14 us, 16 x 5 16.
+  const int span = p.nv <= 8 ? 8 : 32 * ((p.nv + 159) / 160);
+  const int v = (p.nv + span - 1) / span;
+  const int per_block = span <= 32 ? kWarpRowThreads / span : 1;
+  const dim3 grid(static_cast<unsigned>((p.rows + per_block - 1) / per_block));
+  const cudaError_t e = span == 8    ? launch_pdl(norm_kernel<1, 8>, grid, dim3(kWarpRowThreads), 0, s, p)
+                        : span == 32 ? launch_norm<32>(v, grid, dim3(kWarpRowThreads), s, p)
+                                     : launch_norm<0>(v, grid, dim3(span), s, p);
   return check_cuda(e, what);
 }
 
