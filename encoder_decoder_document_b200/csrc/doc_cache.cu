@@ -51,26 +51,44 @@ struct Rows {
   int upr;               // units of a row
 };
 
-// A lane's units: their packed rows and columns, and the cache rows they belong to (-1: none).
+// A lane's units: packed row (relative to the warp's first), column in units, and the cache row (-1: none).
 struct Unit {
-  int64_t row, at;
-  int col;  // in units
+  int row, col;
+  int64_t at;
 };
 
-__device__ __forceinline__ void locate(Unit (&u)[kUnits], const Rows& rows, const CachePages& pages, uint32_t* err) {
+// The warp's units and its first packed row.  Its rows are looked up once, a lane each: with units of 16 columns
+// and rows of at least two units a warp's 128 units are 64 rows at most (two a lane, and only where a row has two
+// units), and every unit takes its row's place from the lane that found it.
+__device__ __forceinline__ int64_t locate(Unit (&u)[kUnits], const Rows& rows, const CachePages& pages,
+                                          uint32_t* err) {
   const int lane = threadIdx.x & 31;
   const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
   const int64_t base = warp * 32 * kUnits;
-  const int64_t r0 = base / rows.upr;
-  const int c0 = static_cast<int>(base - r0 * rows.upr);
+  const int64_t r0 = base >> 32 ? base / rows.upr : static_cast<uint32_t>(base) / static_cast<uint32_t>(rows.upr);
+  int c = static_cast<int>(base - r0 * rows.upr) + lane;
+  const int last = (c - lane + 32 * kUnits - 1) / rows.upr;  // the warp's last row, from r0
+  int64_t mine[2] = {-1, -1};  // cache rows of packed rows r0 + lane and r0 + 32 + lane
+  if (r0 < rows.total) {
+    int d = find_doc_warp(rows.off, rows.n_docs, r0, lane);
+    int64_t begin = __ldg(rows.off + d), end = __ldg(rows.off + d + 1);
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i) u[i].at = -1;
-  if (r0 >= rows.total) return;
-  int d = find_doc_warp(rows.off, rows.n_docs, r0, lane);
-  int64_t begin = __ldg(rows.off + d), end = __ldg(rows.off + d + 1);
-  int64_t r = r0;
-  int64_t held = -1, held_at = -1;  // the last row looked up
-  int c = c0 + lane;
+    for (int k = 0; k < 2; ++k) {
+      const int64_t r = r0 + 32 * k + lane;
+      if (32 * k + lane > last || r >= rows.total) continue;
+      while (r >= end && d + 1 < rows.n_docs) {  // a later document's row (skips empty ones)
+        ++d;
+        begin = end;
+        end = __ldg(rows.off + d + 1);
+      }
+      if (r < begin || r >= end) continue;  // of no document
+      const int64_t i = r - begin + (rows.first ? __ldg(rows.first + d) : 0);
+      if (i >= 0) mine[k] = cache_row(pages, cache_page(pages, d, i), i);
+      if (mine[k] < 0) record_error(err, kErrDeviceArg | kSiteCache);
+    }
+  }
+  __syncwarp();
+  int r = 0;
 #pragma unroll
   for (int i = 0; i < kUnits; ++i, c += 32) {
     while (c >= rows.upr) {
@@ -79,22 +97,13 @@ __device__ __forceinline__ void locate(Unit (&u)[kUnits], const Rows& rows, cons
     }
     u[i].row = r;
     u[i].col = c;
-    if (r != held) {
-      while (r >= end && d + 1 < rows.n_docs) {  // a later document's row (skips empty ones)
-        ++d;
-        begin = end;
-        end = __ldg(rows.off + d + 1);
-      }
-      held = r;
-      held_at = -1;
-      if (r < rows.total && r >= begin && r < end) {
-        const int64_t i_doc = r - begin + (rows.first ? __ldg(rows.first + d) : 0);
-        held_at = i_doc >= 0 ? cache_row(pages, d, i_doc) : -1;
-        if (held_at < 0) record_error(err, kErrDeviceArg | kSiteCache);
-      }
+    u[i].at = __shfl_sync(0xffffffffu, mine[0], r & 31);
+    if (last >= 32) {
+      const int64_t far = __shfl_sync(0xffffffffu, mine[1], r & 31);
+      if (r >= 32) u[i].at = far;
     }
-    u[i].at = held_at;
   }
+  return r0;
 }
 
 // Scale exponent of a group whose largest finite magnitude has these bf16 bits (without the sign).
@@ -127,6 +136,8 @@ __device__ __forceinline__ uint32_t pair_max(uint32_t v) { return max(v, __shfl_
 // Magnitude bits of value k of 16.
 __device__ __forceinline__ uint32_t magnitude(const Words8& x, int k) { return (x.w[k >> 1] >> (16 * (k & 1))) & 0x7fffu; }
 
+__device__ __forceinline__ uint32_t e4m3x2(float2 f) { return __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3); }
+
 template <bool WIDE>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const uint4* __restrict__ src, int64_t ld_src_v,
                                                                const Rows rows, const CachePages pages,
@@ -136,21 +147,23 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const uint4* __re
   pdl_launch_dependents();
   pdl_wait_predecessor();
   Unit u[kUnits];
-  locate(u, rows, pages, err);
+  const uint4* const from = src + locate(u, rows, pages, err) * ld_src_v;
   Words8 x[kUnits];
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) x[i].w[k] = 0;
-    if (u[i].at >= 0) x[i] = load16<WIDE>(src + u[i].row * ld_src_v + u[i].col * 2);
+    if (u[i].at >= 0) x[i] = load16<WIDE>(from + u[i].row * ld_src_v + u[i].col * 2);
   }
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
     const Words8& v = x[i];
     // largest magnitude: bf16 magnitudes order as their bits do
-    uint32_t m2 = 0;
+    constexpr uint32_t kMag = 0x7fff7fffu;
+    uint32_t m2 = v.w[0] & kMag;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) m2 = __vmaxu2(m2, v.w[k] & 0x7fff7fffu);
+    for (int k = 1; k < 7; k += 2) m2 = __vimax3_u16x2(m2, v.w[k] & kMag, v.w[k + 1] & kMag);
+    m2 = __vmaxu2(m2, v.w[7] & kMag);
     uint32_t top = pair_max(max(m2 & 0xffffu, m2 >> 16));
     const bool odd = top >= 0x7f80u;  // an infinity or NaN in the group: the scale is the finite values'
     if (__any_sync(0xffffffffu, odd)) {
@@ -162,24 +175,27 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const uint4* __re
     }
     const int e = group_exp(top);
     const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    float f[16];
+    const F2 inv2 = pair2(inv, inv);
+    uint32_t out[4];
+    if (!odd && e < kCacheMaxExp) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      f[2 * k] = __uint_as_float(v.w[k] << 16) * inv;
-      f[2 * k + 1] = __uint_as_float(v.w[k] & 0xffff0000u) * inv;
-    }
-    if (odd || e >= kCacheMaxExp) {
+      for (int k = 0; k < 4; ++k)
+        out[k] = e4m3x2(split2(mul2(unpack2(v.w[2 * k]), inv2))) |
+                 e4m3x2(split2(mul2(unpack2(v.w[2 * k + 1]), inv2))) << 16;
+    } else {
       const float lim = e >= kCacheMaxExp ? 240.f : 448.f;
 #pragma unroll
-      for (int k = 0; k < 16; ++k)  // an infinity is stored as NaN: no finite code may stand for it
-        f[k] = magnitude(v, k) >= 0x7f80u ? __uint_as_float(0x7fffffffu) : fminf(fmaxf(f[k], -lim), lim);
-    }
-    uint32_t out[4];
+      for (int k = 0; k < 4; ++k) {
+        out[k] = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * k], f[4 * k + 1]), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * k + 2], f[4 * k + 3]), __NV_SATFINITE, __NV_E4M3);
-      out[k] = lo | hi << 16;
+        for (int j = 0; j < 4; ++j) {  // an infinity is stored as NaN: no finite code may stand for it
+          const uint32_t m = magnitude(v, 4 * k + j);
+          const uint32_t w = v.w[2 * k + (j >> 1)];
+          const float f = __uint_as_float(j & 1 ? w & 0xffff0000u : w << 16) * inv;
+          const float g = m >= 0x7f80u ? __uint_as_float(0x7fffffffu) : fminf(fmaxf(f, -lim), lim);
+          out[k] |= (e4m3x2(make_float2(g, 0.f)) & 0xffu) << (8 * j);
+        }
+      }
     }
     if (u[i].at >= 0) {
       *reinterpret_cast<uint4*>(codes + u[i].at * ld_codes + u[i].col * kUnitCols) =
@@ -198,7 +214,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const uint8_t* __r
   pdl_launch_dependents();
   pdl_wait_predecessor();
   Unit u[kUnits];
-  locate(u, rows, pages, err);
+  uint4* const to = dst + locate(u, rows, pages, err) * ld_dst_v;
   uint4 x[kUnits];
   uint32_t s[kUnits];
 #pragma unroll
@@ -210,7 +226,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const uint8_t* __r
 #pragma unroll
   for (int i = 0; i < kUnits; ++i)
     if (u[i].at >= 0)
-      store16<WIDE>(dst + u[i].row * ld_dst_v + u[i].col * 2, e4m3x16_scaled(x[i], scale_bf16x2(s[i])));
+      store16<WIDE>(to + u[i].row * ld_dst_v + u[i].col * 2, e4m3x16_scaled(x[i], scale_bf16x2(s[i])));
 }
 
 }  // namespace

@@ -29,13 +29,16 @@ struct CachePages {
   int32_t shift;   // log2 of the rows of a page
 };
 
-// Cache row of row i of document d; -1 where the table has no such entry or names no page of the cache.
-__device__ __forceinline__ int64_t cache_row(const CachePages& p, int d, int64_t i) {
+// Page that holds row i of document d, -1 where the table has no such entry.
+__device__ __forceinline__ int32_t cache_page(const CachePages& p, int d, int64_t i) {
   const int64_t at = i >> p.shift;
-  if (at >= p.ld) return -1;
-  const int64_t page = __ldg(p.table + d * p.ld + at);
+  return at < p.ld ? __ldg(p.table + d * p.ld + at) : -1;
+}
+
+// Cache row of row i of a document, given its page; -1 where that is no page of the cache.
+__device__ __forceinline__ int64_t cache_row(const CachePages& p, int32_t page, int64_t i) {
   if (page < 0 || page >= p.n_pages) return -1;
-  return (page << p.shift) + (i & ((int64_t{1} << p.shift) - 1));
+  return (static_cast<int64_t>(page) << p.shift) + (i & ((int64_t{1} << p.shift) - 1));
 }
 
 // Two e4m3 codes (low byte first) as a bf16 pair; exact.

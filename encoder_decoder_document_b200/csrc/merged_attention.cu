@@ -1321,7 +1321,7 @@ __global__ void __launch_bounds__(kWidenThreads) cache_widen_kernel(const WidenP
   // lanes 0 .. kRows - 1 look up a row each
   int64_t mine = -1;
   if (lane < kRows && first + lane < nc) {
-    mine = cache_row(p.pages, d, first + lane);
+    mine = cache_row(p.pages, cache_page(p.pages, d, first + lane), first + lane);
     if (mine < 0) record_error(p.err, kErrDeviceArg | kSiteAttention);
   }
   const uint8_t* const codes = p.codes[v] + g * kD + c * 16;
