@@ -1279,15 +1279,17 @@ extern "C" kalm_status kalm_merged_attention(const kalm_bf16* q, int64_t ldq, co
 // about 3,500 cycles of a warp pair on the schedulers that the softmax also needs, more than the 1,700
 // cycles in which the bf16 kernel consumes a tile.
 //
-// Widening kernel: one block per (document, 64 rows, K or V, head).  Bound by latency at these sizes (three
-// dependent loads: the document's offsets, its pages, the codes), by memory for large ones (3 + 1/32 bytes a
-// value).  A warp takes eight rows, two at a time, 16
-// codes a lane; rows up to the next multiple of 64 become zeros, so that
-// the attention's last tile of a document multiplies its masked probabilities with finite values.
+// Widening kernel: a block takes some rows of a document, all heads of K and V: a warp a row at a time, sixteen
+// lanes a head vector (16 codes each), so that its loads are whole lines of the cached row and its stores 1 KB
+// runs.  Rows up to the next multiple of 64 become zeros, so that the attention's last tile of a document multiplies
+// its masked probabilities with finite values.  Bound by latency at these sizes (two dependent loads: the
+// document's offsets and pages, then the codes); 3 + 1/32 bytes a value.
 namespace kalm {
 namespace {
 
 constexpr int kWidenThreads = 256;
+constexpr int kWidenWarps = kWidenThreads / 32;
+constexpr int kWidenAhead = 8;  // head-vector pairs a warp loads before it widens the first
 constexpr int kCrossPad = 64;  // between two documents' rows: room for the last tile's zeros
 
 struct WidenParams {
@@ -1299,49 +1301,63 @@ struct WidenParams {
   __nv_bfloat16* ws;         // [ws_rows][2][n_kv][256]
   int64_t ws_rows;
   int n_kv;
+  int warp_rows;             // rows of a warp
   uint32_t* err;
 };
 
 __global__ void __launch_bounds__(kWidenThreads) cache_widen_kernel(const WidenParams p) {
   pdl_launch_dependents();
   pdl_wait_predecessor();
-  constexpr int kRows = kBKV / (kWidenThreads / 32);  // rows of a warp
-  const int d = blockIdx.y, g = blockIdx.z >> 1, v = blockIdx.z & 1;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int d = blockIdx.y;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kWidenWarps * p.warp_rows + warp * p.warp_rows;
+  // lane l < warp_rows looks up row r0 + l; the page is asked for beside the offsets, before its row is known to exist
+  const int32_t page = lane < p.warp_rows ? cache_page(p.pages, d, r0 + lane) : -1;
   const int64_t c0 = __ldg(p.pool_off + d);
   const int64_t nc = __ldg(p.pool_off + d + 1) - c0;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kBKV;
-  if (r0 >= nc) return;
+  const int64_t end = (nc + kBKV - 1) / kBKV * kBKV;            // rows that the attention's tiles touch
+  if (r0 >= end) return;
   const int64_t to = c0 + static_cast<int64_t>(d) * kCrossPad;  // the document's first workspace row
-  if (c0 < 0 || to + r0 + kBKV > p.ws_rows) {
-    if (threadIdx.x == 0) record_error(p.err, kErrDeviceArg | kSiteAttention);
+  if (c0 < 0 || to + end > p.ws_rows) {
+    if (lane == 0) record_error(p.err, kErrDeviceArg | kSiteAttention);
     return;
   }
-  const int lane = threadIdx.x & 31, half = lane >> 4, c = lane & 15;
-  const int64_t first = r0 + (threadIdx.x >> 5) * kRows;  // the warp's rows
-  // lanes 0 .. kRows - 1 look up a row each
   int64_t mine = -1;
-  if (lane < kRows && first + lane < nc) {
-    mine = cache_row(p.pages, cache_page(p.pages, d, first + lane), first + lane);
+  if (lane < p.warp_rows && r0 + lane < nc) {
+    mine = cache_row(p.pages, page, r0 + lane);
     if (mine < 0) record_error(p.err, kErrDeviceArg | kSiteAttention);
   }
-  const uint8_t* const codes = p.codes[v] + g * kD + c * 16;
-  const uint8_t* const scales = p.scales[v] + g * (kD / kCacheGroup) + (c >> 1);
-  uint4 x[kRows / 2];
-  uint32_t s[kRows / 2];
+  // step q of the warp: row q / n_kv, the head vectors 2 (q % n_kv) and the one after it of [K heads, V heads]
+  const int steps = static_cast<int>(min(static_cast<int64_t>(p.warp_rows), end - r0)) * p.n_kv, c = lane & 15;
+  const uint8_t *const k_codes = p.codes[0], *const v_codes = p.codes[1];
+  const uint8_t *const k_scales = p.scales[0], *const v_scales = p.scales[1];
+  __nv_bfloat16* const dst = p.ws + (to + r0) * p.n_kv * (2 * kD) + lane * 16;
+  int row = 0, vec = lane >> 4;
+  for (int q0 = 0; q0 < steps; q0 += kWidenAhead) {
+    uint4 x[kWidenAhead];
+    uint32_t s[kWidenAhead];
 #pragma unroll
-  for (int i = 0; i < kRows / 2; ++i) {
-    const int64_t at = __shfl_sync(0xffffffffu, mine, 2 * i + half);
-    x[i] = make_uint4(0u, 0u, 0u, 0u);
-    s[i] = 0;
-    if (at >= 0) {
-      x[i] = __ldg(reinterpret_cast<const uint4*>(codes + at * p.ld_codes));
-      s[i] = __ldg(scales + at * p.ld_scales);
+    for (int i = 0; i < kWidenAhead; ++i) {
+      const int64_t at = __shfl_sync(0xffffffffu, mine, row & 31);
+      x[i] = make_uint4(0u, 0u, 0u, 0u);
+      s[i] = 0;
+      if (q0 + i < steps && at >= 0) {
+        const bool v = vec >= p.n_kv;
+        const int g = v ? vec - p.n_kv : vec;
+        x[i] = __ldg(reinterpret_cast<const uint4*>((v ? v_codes : k_codes) + at * p.ld_codes + g * kD) + c);
+        s[i] = __ldg((v ? v_scales : k_scales) + at * p.ld_scales + g * (kD / kCacheGroup) + (c >> 1));
+      }
+      vec += 2;
+      if (vec >= 2 * p.n_kv) {
+        vec = lane >> 4;
+        ++row;
+      }
     }
-  }
-  __nv_bfloat16* const dst = p.ws + ((to + first + half) * 2 + v) * p.n_kv * kD + g * kD + c * 16;
 #pragma unroll
-  for (int i = 0; i < kRows / 2; ++i)
-    stg_words8(dst + static_cast<int64_t>(i) * 4 * p.n_kv * kD, e4m3x16_scaled(x[i], scale_bf16x2(s[i])));
+    for (int i = 0; i < kWidenAhead; ++i)
+      if (q0 + i < steps)
+        stg_words8(dst + static_cast<int64_t>(q0 + i) * (2 * kD), e4m3x16_scaled(x[i], scale_bf16x2(s[i])));
+  }
 }
 
 }  // namespace
@@ -1386,19 +1402,20 @@ extern "C" kalm_status kalm_merged_attention_cache(
                   "kalm_merged_attention_cache: codes must be 16-byte aligned, the strides (%lld, a multiple of 16; "
                   "%lld) cover all heads",
                   (long long)ld_codes, (long long)ld_scales);
-    if (n_docs > 65535 || n_kv > 32767)
-      return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention_cache: n_docs=%d n_kv=%d", n_docs, n_kv);
+    if (n_docs > 65535) return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention_cache: n_docs=%d", n_docs);
   }
   if ((st = ensure_device(nullptr)) != KALM_OK) return st;
   if (any && ld_table > 0) {
-    const int64_t tiles = (ld_table * page_rows + kBKV - 1) / kBKV;  // of the longest document the table can hold
+    const int warp_rows = n_kv >= kWidenAhead ? 1 : kWidenAhead / n_kv;
+    const int64_t rows_max = (ld_table * page_rows + kBKV - 1) / kBKV * kBKV;  // of a document, with its zeros
+    const int block_rows = kWidenWarps * warp_rows;
     const WidenParams wp{{k_codes, v_codes}, {k_scales, v_scales}, ld_codes, ld_scales,
                          CachePages{page_table, ld_table, n_pages, __builtin_ctz(static_cast<unsigned>(page_rows))},
                          pool_off, reinterpret_cast<__nv_bfloat16*>(workspace), workspace_rows, n_kv,
-                         device_error_word()};
+                         warp_rows, device_error_word()};
     st = check_cuda(launch_pdl(cache_widen_kernel,
-                               dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(n_docs),
-                                    static_cast<unsigned>(2 * n_kv)),
+                               dim3(static_cast<unsigned>((rows_max + block_rows - 1) / block_rows),
+                                    static_cast<unsigned>(n_docs)),
                                dim3(kWidenThreads), 0, static_cast<cudaStream_t>(stream), wp),
                     "launch cache_widen_kernel");
     if (st != KALM_OK) return st;
