@@ -29,6 +29,7 @@ __all__ = [
 HEAD_DIM = 256
 MAX_QUERY_TOKENS = 512  # KALM_MAX_QUERY_TOKENS
 CACHE_GROUP = 32  # KALM_CACHE_GROUP: columns of a cached row that share a scale
+CACHE_FEW_ROWS = 8  # KALM_CACHE_FEW_ROWS: packed rows up to which the cache attention takes no workspace
 
 
 def _stream(stream: Optional[torch.cuda.Stream]) -> int:
@@ -383,7 +384,8 @@ def kalm_merged_attention_cache(q: torch.Tensor, k_self: torch.Tensor, v_self: t
     the other arguments as kalm_merged_attention.
 
     workspace: bf16 scratch [>= kalm_merged_attention_cache_rows(cached rows, n_docs)][2 * n_kv * head_dim];
-    None allocates one for this call, for as many rows as the page table has places."""
+    None allocates one for this call, for as many rows as the page table has places.  Calls of at most
+    CACHE_FEW_ROWS packed rows a KV head (max_q * n_q / n_kv) use none."""
     where = "kalm_merged_attention_cache"
     bf16, u8 = torch.bfloat16, torch.uint8
     dev = _device(where, q)
@@ -410,21 +412,24 @@ def kalm_merged_attention_cache(q: torch.Tensor, k_self: torch.Tensor, v_self: t
         if order.dtype is not torch.int32 or order.get_device() != dev or order.numel() < items or \
                 not order.is_contiguous():
             _refuse(where, "order", order, torch.int32, dev, f"expected at least the call's {items} work items")
-    if workspace is None:
+    ws, ws_rows = None, 0
+    if workspace is None and max_q * n_q > CACHE_FEW_ROWS * n_kv:
         shape = (n_docs * (ld_table * page_rows + 64), 2 * width)  # every place of the table, see the rows helper below
         if stream is None:
             workspace = torch.empty(shape, dtype=bf16, device=q.device)
         else:
             with torch.cuda.stream(stream):  # the allocator hands memory out per stream
                 workspace = torch.empty(shape, dtype=bf16, device=q.device)
-    elif _mat(where, "workspace", workspace, bf16, dev, -1, 2 * width) != 2 * width:
+    elif workspace is not None and _mat(where, "workspace", workspace, bf16, dev, -1, 2 * width) != 2 * width:
         raise KalmError(1, where, "the workspace must be contiguous")
+    if workspace is not None:
+        ws, ws_rows = workspace.data_ptr(), workspace.shape[0]
     call(where, q.data_ptr(), ldq, k_self.data_ptr(), v_self.data_ptr(), ld_self, k_codes.data_ptr(),
          v_codes.data_ptr(), ld_codes, k_scales.data_ptr(), v_scales.data_ptr(), ld_scales, page_table.data_ptr(),
          ld_table, page_rows, n_pages, _vec(where, "q_off", q_off, torch.int64, dev, n_docs + 1),
          _vec(where, "in_off", in_off, torch.int64, dev, n_docs), rows, pool_off.data_ptr(), n_docs, max_q, total_q,
          n_q, n_kv, head_dim, head_dim ** -0.5 if scale is None else scale, 1 if last_tile_only else 0,
-         None if order is None else order.data_ptr(), workspace.data_ptr(), workspace.shape[0], out.data_ptr(), ldo,
+         None if order is None else order.data_ptr(), ws, ws_rows, out.data_ptr(), ldo,
          None if lse is None else lse.data_ptr(), _stream(stream))
 
 

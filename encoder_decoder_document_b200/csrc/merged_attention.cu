@@ -45,6 +45,7 @@
 #include <cmath>
 #include <mutex>
 
+#include "cache_rows_attention.h"
 #include "kalm.h"
 #include "kalm_cache.cuh"
 #include "kalm_internal.h"
@@ -1377,7 +1378,10 @@ extern "C" kalm_status kalm_merged_attention_cache(
     const int32_t* order, kalm_bf16* workspace, int64_t workspace_rows, kalm_bf16* out, int64_t ldo, float* lse,
     kalm_stream_t stream) {
   const int64_t width = static_cast<int64_t>(n_kv) * kD;
-  const int64_t rows = ld_table > 0 ? workspace_rows : 0;  // no pages, nothing cached
+  // few packed rows a KV head: no tensor-core tiles, no workspace
+  const bool few = n_kv > 0 && n_q > 0 && n_q % n_kv == 0 && max_q >= 0 &&
+                   static_cast<int64_t>(max_q) * (n_q / n_kv) <= KALM_CACHE_FEW_ROWS;
+  const int64_t rows = ld_table > 0 && !few ? workspace_rows : 0;  // no pages: nothing cached
   kalm_status st = check_attention(q, ldq, k_self, v_self, ld_self, workspace, workspace, 2 * width, q_off, in_off,
                                    total_in, pool_off, n_docs, max_q, total_q, rows, n_q, n_kv, head_dim, scale, out,
                                    ldo);
@@ -1392,9 +1396,9 @@ extern "C" kalm_status kalm_merged_attention_cache(
   if (any && ld_table > 0) {
     if (!page_table || (n_pages > 0 && (!k_codes || !v_codes || !k_scales || !v_scales)))
       return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention_cache: NULL pointer");
-    if (workspace_rows == 0)
+    if (!few && workspace_rows == 0)
       return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention_cache: no workspace");
-    if (reinterpret_cast<uintptr_t>(workspace) & 31u)
+    if (!few && reinterpret_cast<uintptr_t>(workspace) & 31u)
       return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention_cache: the workspace must be 32-byte aligned");
     if (!aligned16(k_codes) || !aligned16(v_codes) || ld_codes % 16 || ld_codes < width ||
         ld_scales < width / kCacheGroup)
@@ -1405,6 +1409,35 @@ extern "C" kalm_status kalm_merged_attention_cache(
     if (n_docs > 65535) return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention_cache: n_docs=%d", n_docs);
   }
   if ((st = ensure_device(nullptr)) != KALM_OK) return st;
+  if (any && few) {
+    CacheRowsParams p{};
+    p.q = reinterpret_cast<const __nv_bfloat16*>(q);
+    p.k_self = reinterpret_cast<const __nv_bfloat16*>(k_self);
+    p.v_self = reinterpret_cast<const __nv_bfloat16*>(v_self);
+    p.k_codes = k_codes;
+    p.v_codes = v_codes;
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    p.ldq = ldq;
+    p.ld_self = ld_self;
+    p.ld_codes = ld_codes;
+    p.ld_scales = ld_scales;
+    p.ldo = ldo;
+    p.pages = CachePages{page_table, ld_table, n_pages, __builtin_ctz(static_cast<unsigned>(page_rows))};
+    p.q_off = q_off;
+    p.in_off = in_off;
+    p.pool_off = pool_off;
+    p.total_in = in_off ? total_in : total_q;
+    p.n_q = n_q;
+    p.n_kv = n_kv;
+    p.G = n_q / n_kv;
+    p.max_q = max_q;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.out = reinterpret_cast<__nv_bfloat16*>(out);
+    p.lse = lse;
+    p.err = device_error_word();
+    return launch_cache_rows_attention(p, n_docs, static_cast<cudaStream_t>(stream));
+  }
   if (any && ld_table > 0) {
     const int warp_rows = n_kv >= kWidenAhead ? 1 : kWidenAhead / n_kv;
     const int64_t rows_max = (ld_table * page_rows + kBKV - 1) / kBKV * kBKV;  // of a document, with its zeros

@@ -485,6 +485,7 @@ kalm_status kalm_linear_rope(const kalm_bf16* x, int64_t ldx, const kalm_bf16* w
  * error word.
  * ------------------------------------------------------------------------- */
 #define KALM_CACHE_GROUP 32
+#define KALM_CACHE_FEW_ROWS 8
 #define KALM_CACHE_MIN_PAGE_ROWS 8
 #define KALM_CACHE_MAX_PAGE_ROWS 1024
 
@@ -520,7 +521,9 @@ kalm_status kalm_cache_read(const uint8_t* codes, int64_t ld_codes, const uint8_
  * numbers exactly, so the result is that of kalm_merged_attention over the rows
  * that kalm_cache_read returns.  Same passages as kalm_merged_attention.  Two
  * launches: the call's cached rows are widened to bf16 into the workspace, once for
- * all their query tiles, and attended over from there.
+ * all their query tiles, and attended over from there.  Calls of few rows (max_q *
+ * n_q / n_kv <= KALM_CACHE_FEW_ROWS, as in a step of one position) are one launch
+ * that reads the codes itself and neither needs nor touches the workspace.
  *
  * q .. total_in, max_q, total_q, n_q .. lse   as kalm_merged_attention (order from
  *          kalm_attention_schedule for the same offsets and sizes, or NULL)
@@ -535,7 +538,7 @@ kalm_status kalm_cache_read(const uint8_t* codes, int64_t ld_codes, const uint8_
  *          kalm_merged_attention_cache_rows(pool_off[n_docs], n_docs) rows (a
  *          document that reaches past it is flagged); scratch, no contents are
  *          kept from call to call.  Calls that overlap on the GPU need their own.
- *          NULL with 0 rows where ld_table is 0 (nothing cached).
+ *          NULL with 0 rows where ld_table is 0 (nothing cached) or the rows are few.
  * What lies behind a document's last cached row has no influence, NaN and
  * infinities included.  As with kalm_merged_attention, the self rows are to be
  * finite: a NaN or infinity in a V row reaches the query tiles (128 / (n_q / n_kv)

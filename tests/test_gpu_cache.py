@@ -292,7 +292,8 @@ def plain_attention(a, scale=1 / 16, in_off=None):
     return out, lse, vmax
 
 
-def run_attention(kalm, a, scale=1 / 16, order=None, in_off=None, last=False, poison=False, stream=None, page_table=None):
+def run_attention(kalm, a, scale=1 / 16, order=None, in_off=None, last=False, poison=False, stream=None, page_table=None,
+                  max_q=None):
     d, n_q, n_kv = 256, a["n_q"], a["n_kv"]
     rows = a["q"].shape[0]
     q_off, p_off = i64(a["q_off"]), i64(a["p_off"])
@@ -315,7 +316,8 @@ def run_attention(kalm, a, scale=1 / 16, order=None, in_off=None, last=False, po
     ksc, vsc = scales[:, win // 32:(win + w) // 32], scales[:, (win + w) // 32:]
     kalm.kalm_merged_attention_cache(
         qkv[:, :n_q * d], qkv[:, n_q * d:n_q * d + w], qkv[:, n_q * d + w:], kc, ksc, vc, vsc,
-        i32(a["table"]) if page_table is None else page_table, a["page_rows"], q_off, p_off, max(a["lq"]), n_q, n_kv, out,
+        i32(a["table"]) if page_table is None else page_table, a["page_rows"], q_off, p_off, max_q or max(a["lq"]),
+        n_q, n_kv, out,
         scale, lse, in_off=None if in_off is None else i64(in_off), last_tile_only=last,
         order=order(q_off, p_off) if order else None, stream=stream)
     if stream is not None:
@@ -343,6 +345,16 @@ SHAPES = [
     ([40, 130], [20, 70], 8, 1, 128),                      # 8 query heads per KV head
     ([5, 9], [0, 0], 4, 1, 8),                             # nothing cached in the whole batch
     ([3] * 200, list(range(0, 200)), 4, 1, 16),            # more items than CTAs
+    # up to eight packed rows a KV head: the few-row form, at each of its row counts
+    ([1] * 5, [0, 1, 63, 64, 300], 2, 2, 8),               # 1 row
+    ([1, 0, 1], [17, 5, 1024], 4, 2, 16),                  # 2 rows, a document without decoder rows
+    ([2, 1, 2], [9, 130, 0], 1, 1, 64),                    # 2 rows of one head: causal self keys
+    ([1] * 160, [7 * i % 131 for i in range(160)], 4, 1, 32),
+    ([4, 3, 1, 2], [1000, 33, 64, 8], 1, 1, 128),          # 4 rows, 4 positions
+    ([2, 1], [70, 257], 8, 4, 16),
+    ([1, 1], [256, 65], 8, 1, 64),                         # 8 rows, one position of 8 heads
+    ([8, 5, 0, 1], [40, 0, 3, 600], 2, 2, 8),              # 8 positions
+    ([2, 2, 1], [5, 64, 513], 4, 1, 64),
 ]
 
 
@@ -352,3 +364,30 @@ def test_attention(kalm, lq, nc, n_q, n_kv, page_rows):
     got, lse = run_attention(kalm, a, poison=True)
     assert kalm.kalm_check_device_errors() == 0
     check(got, lse, *plain_attention(a))
+
+
+@pytest.mark.parametrize("lq,nc,n_q,n_kv", [([1] * 30, list(range(30)), 4, 1), ([2, 1], [300, 64], 8, 2)])
+def test_few_rows_agree_with_many(kalm, lq, nc, n_q, n_kv):
+    """The two forms of the attention on the same documents: a call sized for more positions takes the other one."""
+    a = attention(np.random.default_rng(n_q), lq, nc, n_q, n_kv, 32)
+    few, few_lse = run_attention(kalm, a)
+    many, many_lse = run_attention(kalm, a, max_q=64)
+    want, want_lse, vmax = plain_attention(a)
+    check(few, few_lse, want, want_lse, vmax)
+    check(many, many_lse, want, want_lse, vmax)
+    # nothing is rounded before the few-row form's output: half a bf16 step and fp32 effects
+    assert (np.abs(few - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -15 * vmax[..., None]).all()
+
+
+def test_few_rows_of_nan_free_documents(kalm):
+    """NaN in pages that no attended row names, and scores that jump by far more than fp32's exponent range allows."""
+    rng = np.random.default_rng(77)
+    a = attention(rng, [1, 1], [100, 40], 4, 1, 16)
+    a["scales"][cached_rows(a, 0)[50], :8] += 12   # one key of document 0 dominates
+    a["scales"][cached_rows(a, 1)[0], :8] += 14
+    got, lse = run_attention(kalm, a, poison=True)
+    want, want_lse, vmax = plain_attention(a)
+    assert np.isfinite(got).all() and (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -12 * vmax[..., None]).all()
+    # logits of up to 1e4 in fp32: relative 2^-20
+    assert (np.abs(lse - want_lse) <= 2.0 ** -20 * np.abs(want_lse) + 1e-4).all()
+    assert kalm.kalm_check_device_errors() == 0
