@@ -1,8 +1,15 @@
 // Merged attention over an 8-bit cache for a few decoder rows: a document's decoder positions times the query
-// heads of a KV head are at most KALM_CACHE_FEW_ROWS packed rows (one position with up to eight heads a KV head, as in
+// heads of a KV head are at most KALM_CACHE_FEW_ROWS packed rows (one position with up to four heads a KV head, as in
 // a step that adds a token).  Same result as the tensor-core path of kalm_merged_attention_cache, one launch,
-// no workspace: there is too little arithmetic for tensor-core tiles (4 rows of 128 would be real), and what
-// counts is the latency of few dependent loads.
+// no workspace: there is too little arithmetic for tensor-core tiles (4 rows of 128 would be real).
+//
+// Against the tensor-core path (us; one position per document, documents of 16 to 256 cached rows, one KV head):
+//   documents      1 row          2 rows         4 rows         8 rows
+//   1              5.1 / 13.3     5.8 / 13.3     8.0 / 13.3     11.8 / 13.3
+//   100            8.2 / 19.6     9.6 / 19.6     13.1 / 19.6    19.3 / 19.7
+//   1,000          44 / 112       52 / 112       76 / 112       115 / 112
+// so four rows are the border.  Bound by the latency of the dependent loads (offsets, pages, codes) for few
+// documents and by the fp32 pipe's instructions for many (100 documents: 6.9 MB in 13.1 us).
 //
 // One block per (document, KV head), eight warps.  For each packed row r and visible key j
 //   s = scale * q_r . k_j;   out_r = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m)
@@ -29,47 +36,44 @@ namespace {
 constexpr int kHeadDim = 256;
 constexpr int kWarps = 8;
 
-__device__ __forceinline__ void unpack_bf16x8(const uint4& v, float (&f)[8]) {
+__device__ __forceinline__ void unpack_bf16x8(const uint4& v, F2 (&f)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    f[2 * k] = __uint_as_float(w[k] << 16);
-    f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-  }
+  for (int k = 0; k < 4; ++k) f[k] = unpack2(w[k]);
 }
 
-__device__ __forceinline__ void unpack_e4m3x8(const uint2& v, float (&f)[8]) {
+__device__ __forceinline__ void unpack_e4m3x8(const uint2& v, F2 (&f)[4]) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const uint32_t two = ((k & 2 ? v.y : v.x) >> (16 * (k & 1))) & 0xffffu;
     const float2 g = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3)));
-    f[2 * k] = g.x;
-    f[2 * k + 1] = g.y;
+    f[k] = pair2(g.x, g.y);
   }
 }
 
 constexpr int log2_of(int n) { return n <= 1 ? 0 : 1 + log2_of(n / 2); }
 
-// R packed rows (a power of two), KEYS keys at a time; R * KEYS <= 32.
+// R packed rows (1, 2 or 4), KEYS keys at a time; R * KEYS <= 32.  (4 keys at a time: 9.2, 10.6, 13.3 us for 1, 2, 4 rows of 100
+// documents against 8.2, 9.6, 13.1.)
 template <int R>
 struct Few {
-  static constexpr int KEYS = R <= 4 ? 8 : 32 / R;
+  static constexpr int KEYS = 8;
   static constexpr int N = R * KEYS;              // scores of a group of keys
   static constexpr int DUP = 5 - log2_of(N);      // the score of (key j, row r) is in lanes (j * R + r) << DUP and on
 };
 
 template <int R>
 struct State {
-  float q[R][8];    // this lane's 8 columns of each row, times scale * log2(e)
-  float acc[R][8];  // sum of p * v, relative to the row's maximum
-  float m, l;       // of this lane's row (lane >> DUP) % R: running maximum (base 2), this lane's keys' sum
+  F2 q[R][4];    // this lane's 8 columns of each row, times scale * log2(e)
+  F2 acc[R][4];  // sum of p * v, relative to the row's maximum
+  float m, l;    // of this lane's row (lane >> DUP) % R: running maximum (base 2), this lane's keys' sum
 };
 
 // One group of keys: their 8 columns in this lane (k, v as fp32 numbers, times ks, vs), `seen`: whether this
 // lane's (key, row) counts.
 template <int R>
-__device__ __forceinline__ void attend(State<R>& st, const float (&k)[Few<R>::KEYS][8], const float (&ks)[Few<R>::KEYS],
-                                       const float (&v)[Few<R>::KEYS][8], const float (&vs)[Few<R>::KEYS], bool seen,
+__device__ __forceinline__ void attend(State<R>& st, const F2 (&k)[Few<R>::KEYS][4], const float (&ks)[Few<R>::KEYS],
+                                       const F2 (&v)[Few<R>::KEYS][4], const float (&vs)[Few<R>::KEYS], bool seen,
                                        int lane) {
   constexpr int KEYS = Few<R>::KEYS, N = Few<R>::N, DUP = Few<R>::DUP;
   float part[N];
@@ -77,10 +81,11 @@ __device__ __forceinline__ void attend(State<R>& st, const float (&k)[Few<R>::KE
   for (int j = 0; j < KEYS; ++j)
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float s = 0.f;
+      F2 s = mul2(k[j][0], st.q[r][0]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s = fmaf(k[j][e], st.q[r][e], s);
-      part[j * R + r] = s * ks[j];
+      for (int e = 1; e < 4; ++e) s = fma2(k[j][e], st.q[r][e], s);
+      const float2 both = split2(s);
+      part[j * R + r] = (both.x + both.y) * ks[j];
     }
   // halve: after the step with mask b the lanes with that bit hold the upper half of the sums
   int b = 16;
@@ -116,7 +121,7 @@ __device__ __forceinline__ void attend(State<R>& st, const float (&k)[Few<R>::KE
     for (int r = 0; r < R; ++r) {
       const float a = __shfl_sync(0xffffffffu, alpha, r << DUP);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) st.acc[r][e] *= a;
+      for (int e = 0; e < 4; ++e) st.acc[r][e] = mul2(st.acc[r][e], pair2(a, a));
     }
   }
 #pragma unroll
@@ -125,7 +130,7 @@ __device__ __forceinline__ void attend(State<R>& st, const float (&k)[Few<R>::KE
     for (int r = 0; r < R; ++r) {
       const float pj = __shfl_sync(0xffffffffu, p, (j * R + r) << DUP) * vs[j];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) st.acc[r][e] = fmaf(pj, v[j][e], st.acc[r][e]);
+      for (int e = 0; e < 4; ++e) st.acc[r][e] = fma2(pair2(pj, pj), v[j][e], st.acc[r][e]);
     }
 }
 
@@ -209,9 +214,9 @@ __global__ void __launch_bounds__(kWarps * 32) cache_rows_attention_kernel(const
                                           static_cast<int64_t>(head * p.G + r % p.G) * kHeadDim + lane * 8);
     unpack_bf16x8(x, st.q[r]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      st.q[r][e] *= p.scale_log2;
-      st.acc[r][e] = 0.f;
+    for (int e = 0; e < 4; ++e) {
+      st.q[r][e] = mul2(st.q[r][e], pair2(p.scale_log2, p.scale_log2));
+      st.acc[r][e] = 0;  // a pair of zeros
     }
   }
   const int my = lane >> DUP;             // this lane's (key, row) of a group
@@ -220,7 +225,8 @@ __global__ void __launch_bounds__(kWarps * 32) cache_rows_attention_kernel(const
   // the last warp takes the self keys (at most R), the row's position and those before it
   if (warp == kWarps - 1) {
     for (int j0 = 0; j0 < static_cast<int>(lq); j0 += KEYS) {
-      float k[KEYS][8], v[KEYS][8], one[KEYS];
+      F2 k[KEYS][4], v[KEYS][4];
+      float one[KEYS];
 #pragma unroll
       for (int j = 0; j < KEYS; ++j) {
         uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
@@ -241,7 +247,8 @@ __global__ void __launch_bounds__(kWarps * 32) cache_rows_attention_kernel(const
     first += step;
     load_group<R>(next, p, head, first, nc, page, lane);
     page = group_page<R>(p, d, first + step, nc, lane);
-    float k[KEYS][8], v[KEYS][8], ks[KEYS], vs[KEYS];
+    F2 k[KEYS][4], v[KEYS][4];
+    float ks[KEYS], vs[KEYS];
 #pragma unroll
     for (int j = 0; j < KEYS; ++j) {
       unpack_e4m3x8(cur.k[j], k[j]);
@@ -263,8 +270,9 @@ __global__ void __launch_bounds__(kWarps * 32) cache_rows_attention_kernel(const
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     float4* to = reinterpret_cast<float4*>(acc_s + (warp * R + r) * kHeadDim + lane * 8);
-    to[0] = make_float4(st.acc[r][0], st.acc[r][1], st.acc[r][2], st.acc[r][3]);
-    to[1] = make_float4(st.acc[r][4], st.acc[r][5], st.acc[r][6], st.acc[r][7]);
+    const float2 a = split2(st.acc[r][0]), b = split2(st.acc[r][1]), c = split2(st.acc[r][2]), e = split2(st.acc[r][3]);
+    to[0] = make_float4(a.x, a.y, b.x, b.y);
+    to[1] = make_float4(c.x, c.y, e.x, e.y);
   }
   __syncthreads();
   // join the warps: thread t has columns 2 (t % 128), rows t / 128, + 2, ...
@@ -305,21 +313,14 @@ cudaError_t launch_rows(const CacheRowsParams& p, int n_docs, cudaStream_t s) {
 
 }  // namespace
 
-kalm_status setup_cache_rows_kernels() {
-  return check_cuda(cudaFuncSetAttribute(cache_rows_attention_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         few_smem<8>()),
-                    "cudaFuncSetAttribute(cache_rows_attention_kernel)");
-}
-
 kalm_status launch_cache_rows_attention(const CacheRowsParams& p, int32_t n_docs, cudaStream_t stream) {
   const int rows = p.max_q * p.G;
   if (static_cast<int64_t>(n_docs) * p.n_kv > INT32_MAX)
     return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention_cache: too many work items");
-  static_assert(KALM_CACHE_FEW_ROWS == 8 && few_smem<4>() <= 48 * 1024, "row counts and shared memory");
+  static_assert(KALM_CACHE_FEW_ROWS == 4 && few_smem<4>() <= 48 * 1024, "row counts and shared memory");
   return check_cuda(rows <= 1   ? launch_rows<1>(p, n_docs, stream)
                     : rows <= 2 ? launch_rows<2>(p, n_docs, stream)
-                    : rows <= 4 ? launch_rows<4>(p, n_docs, stream)
-                                : launch_rows<8>(p, n_docs, stream),
+                                : launch_rows<4>(p, n_docs, stream),
                     "launch cache_rows_attention_kernel");
 }
 

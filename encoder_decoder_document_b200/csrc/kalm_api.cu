@@ -57,7 +57,6 @@ kalm_status check_cuda(cudaError_t e, const char* what) {
 // Per-kernel set-up hooks defined in the other translation units.
 kalm_status setup_linear_kernels();
 kalm_status setup_attention_kernels();
-kalm_status setup_cache_rows_kernels();
 
 kalm_status ensure_device(int* device_out) {
   int dev = -1;
@@ -104,7 +103,6 @@ kalm_status ensure_device(int* device_out) {
   }
   if ((st = setup_linear_kernels()) != KALM_OK) return st;
   if ((st = setup_attention_kernels()) != KALM_OK) return st;
-  if ((st = setup_cache_rows_kernels()) != KALM_OK) return st;
   s.ok = true;
   s.ready.store(true, std::memory_order_release);
   return KALM_OK;

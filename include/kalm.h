@@ -485,7 +485,7 @@ kalm_status kalm_linear_rope(const kalm_bf16* x, int64_t ldx, const kalm_bf16* w
  * error word.
  * ------------------------------------------------------------------------- */
 #define KALM_CACHE_GROUP 32
-#define KALM_CACHE_FEW_ROWS 8
+#define KALM_CACHE_FEW_ROWS 4
 #define KALM_CACHE_MIN_PAGE_ROWS 8
 #define KALM_CACHE_MAX_PAGE_ROWS 1024
 

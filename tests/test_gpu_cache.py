@@ -345,7 +345,7 @@ SHAPES = [
     ([40, 130], [20, 70], 8, 1, 128),                      # 8 query heads per KV head
     ([5, 9], [0, 0], 4, 1, 8),                             # nothing cached in the whole batch
     ([3] * 200, list(range(0, 200)), 4, 1, 16),            # more items than CTAs
-    # up to eight packed rows a KV head: the few-row form, at each of its row counts
+    # up to four packed rows a KV head: the few-row form, at each of its row counts, and the first beyond it
     ([1] * 5, [0, 1, 63, 64, 300], 2, 2, 8),               # 1 row
     ([1, 0, 1], [17, 5, 1024], 4, 2, 16),                  # 2 rows, a document without decoder rows
     ([2, 1, 2], [9, 130, 0], 1, 1, 64),                    # 2 rows of one head: causal self keys
@@ -366,7 +366,7 @@ def test_attention(kalm, lq, nc, n_q, n_kv, page_rows):
     check(got, lse, *plain_attention(a))
 
 
-@pytest.mark.parametrize("lq,nc,n_q,n_kv", [([1] * 30, list(range(30)), 4, 1), ([2, 1], [300, 64], 8, 2)])
+@pytest.mark.parametrize("lq,nc,n_q,n_kv", [([1] * 30, list(range(30)), 4, 1), ([2, 1], [300, 64], 4, 2)])
 def test_few_rows_agree_with_many(kalm, lq, nc, n_q, n_kv):
     """The two forms of the attention on the same documents: a call sized for more positions takes the other one."""
     a = attention(np.random.default_rng(n_q), lq, nc, n_q, n_kv, 32)
