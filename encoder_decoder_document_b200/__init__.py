@@ -86,6 +86,13 @@ def _mat(where: str, name: str, t: torch.Tensor, dtype: torch.dtype, dev: int, r
     return ld if shape[0] > 1 else -(-shape[1] // 16) * 16
 
 
+def _pair(where: str, name: str, k: torch.Tensor, v: torch.Tensor) -> None:
+    """The V tensor of a K / V pair is laid out as its (checked) K."""
+    if v.dtype is not k.dtype or v.device != k.device or v.shape != k.shape or v.stride() != k.stride():
+        raise KalmError(1, where, f"{name}: K is {k.dtype} {tuple(k.shape)} with strides {k.stride()} on {k.device}, V "
+                                  f"{v.dtype} {tuple(v.shape)} with strides {v.stride()} on {v.device}")
+
+
 def _vec(where: str, name: str, t: Optional[torch.Tensor], dtype: torch.dtype, dev: int, n: int) -> Optional[int]:
     """Address of a contiguous vector of n values (None passes)."""
     if t is None:
@@ -387,17 +394,15 @@ def kalm_merged_attention_cache(q: torch.Tensor, k_self: torch.Tensor, v_self: t
     None allocates one for this call, for as many rows as the page table has places.  Calls of at most
     CACHE_FEW_ROWS packed rows a KV head (max_q * n_q / n_kv) use none."""
     where = "kalm_merged_attention_cache"
-    bf16, u8 = torch.bfloat16, torch.uint8
+    bf16 = torch.bfloat16
     dev = _device(where, q)
     width, rows = n_kv * head_dim, q.shape[0]
     n_docs, ld_table, n_pages, ld_codes, ld_scales = _cache_args(where, dev, pool_off, page_table, page_rows, k_codes,
                                                                  k_scales, width)
-    cached = n_pages * page_rows
     ld_self = _mat(where, "k_self", k_self, bf16, dev, rows, width)
-    if _mat(where, "v_self", v_self, bf16, dev, rows, width) != ld_self or \
-            _mat(where, "v_codes", v_codes, u8, dev, cached, width) != ld_codes or \
-            _mat(where, "v_scales", v_scales, u8, dev, cached, width // CACHE_GROUP) != ld_scales:
-        raise KalmError(1, where, "K and V must share their row strides")
+    _pair(where, "self rows", k_self, v_self)
+    _pair(where, "codes", k_codes, v_codes)
+    _pair(where, "scales", k_scales, v_scales)
     ldq = _mat(where, "q", q, bf16, dev, rows, n_q * head_dim)
     ldo = _mat(where, "out", out, bf16, dev, -1, n_q * head_dim)
     if total_q is None:
@@ -408,7 +413,8 @@ def kalm_merged_attention_cache(q: torch.Tensor, k_self: torch.Tensor, v_self: t
                             lse.shape[0] < total_q or lse.shape[1] != n_q or not lse.is_contiguous()):
         _refuse(where, "lse", lse, torch.float32, dev, f"expected a contiguous [{total_q}][{n_q}] tensor")
     if order is not None:
-        items = kalm_attention_items(n_docs, max_q, n_q, n_kv, last_tile_only)
+        tile = max(128 * n_kv // n_q, 1) if n_q > 0 else 1  # positions of a query tile, as kalm_attention_items counts them
+        items = n_docs * n_kv * (1 if last_tile_only else -(-max_q // tile))
         if order.dtype is not torch.int32 or order.get_device() != dev or order.numel() < items or \
                 not order.is_contiguous():
             _refuse(where, "order", order, torch.int32, dev, f"expected at least the call's {items} work items")

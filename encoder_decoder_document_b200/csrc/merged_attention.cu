@@ -1212,10 +1212,7 @@ kalm_status launch_attention(const kalm_bf16* q, int64_t ldq, const kalm_bf16* k
   const int64_t items = static_cast<int64_t>(last_tile_only ? 1 : prm.tiles_per_doc) * n_docs * n_kv;
   if (items > INT32_MAX) return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention: too many work items");
   prm.n_items = static_cast<int>(items);
-  int sms = 0, dev = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (sms <= 0) sms = 148;
+  const int sms = num_sms();
   const int64_t grid = items < sms ? items : sms;  // persistent: one CTA per SM
   if (!op) {
     return check_cuda(launch_pdl(merged_attention_kernel<false>, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
