@@ -391,3 +391,279 @@ def test_few_rows_of_nan_free_documents(kalm):
     # logits of up to 1e4 in fp32: relative 2^-20
     assert (np.abs(lse - want_lse) <= 2.0 ** -20 * np.abs(want_lse) + 1e-4).all()
     assert kalm.kalm_check_device_errors() == 0
+
+
+# ------------------------------------------------------------------ the ways a program calls them
+def test_attention_shared_inputs_order_and_last_tile(kalm):
+    """Documents that share their decoder rows, a work order, and the last-tile-only mode."""
+    n_q, n_kv, lq, nc = 4, 1, 70, [5, 130, 0, 64]
+    rng = np.random.default_rng(34)
+    a = attention(rng, [lq] * 4, nc, n_q, n_kv, 16)
+    for k in ("q", "ks", "vs"):
+        a[k] = a[k][:lq]
+    in_off = [0] * 4
+    want, want_lse, vmax = plain_attention(a, in_off=in_off)
+
+    def order(q_off, p_off):
+        o = torch.empty(kalm.kalm_attention_items(4, lq, n_q, n_kv), dtype=torch.int32, device="cuda")
+        kalm.kalm_attention_schedule(q_off, p_off, lq, n_q, n_kv, o)
+        return o
+
+    got, lse = run_attention(kalm, a, in_off=in_off, poison=True)
+    check(got, lse, want, want_lse, vmax)
+    again, _ = run_attention(kalm, a, in_off=in_off, order=order)
+    np.testing.assert_array_equal(again, got)
+    last, _ = run_attention(kalm, a, in_off=in_off, last=True)
+    first = (lq - 1) // 32 * 32  # 128 / 4 positions a tile
+    for d in range(4):
+        np.testing.assert_array_equal(last[d * lq + first:(d + 1) * lq], got[d * lq + first:(d + 1) * lq])
+        assert np.isnan(last[d * lq:d * lq + first]).all()
+    assert kalm.kalm_check_device_errors() == 0
+
+
+def test_attention_equals_the_uncached_kernel_over_read_rows(kalm):
+    """Bit for bit kalm_merged_attention over what kalm_cache_read returns (the tensor-core form)."""
+    lq, nc, n_q, n_kv = [64, 7, 130], [100, 256, 33], 8, 4
+    a = attention(np.random.default_rng(8), lq, nc, n_q, n_kv, 8)
+    got, lse = run_attention(kalm, a)
+    w, d = n_kv * 256, 256
+    codes, scales = torch.from_numpy(a["codes"]).cuda(), torch.from_numpy(a["scales"]).cuda()
+    kv = torch.empty(sum(nc), 2 * w, dtype=torch.bfloat16, device="cuda")
+    kalm.kalm_cache_read(codes, scales, i64(a["p_off"]), i32(a["table"]), 8, kv)
+    r = sum(lq)
+    qkv = torch.cat([f64_to_dev(a[k].reshape(r, -1)) for k in ("q", "ks", "vs")], 1)
+    out = torch.empty(r, n_q * d, dtype=torch.bfloat16, device="cuda")
+    ref_lse = torch.empty(r, n_q, device="cuda")
+    kalm.kalm_merged_attention(qkv[:, :n_q * d], qkv[:, n_q * d:n_q * d + w], qkv[:, n_q * d + w:], kv[:, :w], kv[:, w:],
+                               i64(a["q_off"]), i64(a["p_off"]), max(lq), n_q, n_kv, out, 1 / 16, ref_lse)
+    np.testing.assert_array_equal(from_dev(out).reshape(got.shape), got)
+    np.testing.assert_array_equal(ref_lse.cpu().numpy().astype(np.float64), lse)
+
+
+def test_attention_bad_pages_and_short_workspace(kalm):
+    """Rows without a page count as zeros and are flagged, in both forms; a workspace that is too short is flagged."""
+    for lq in ([40, 3], [1, 1]):
+        a = attention(np.random.default_rng(9), lq, [70, 20], 4, 1, 16)
+        table = a["table"].copy()
+        table[0, 2], table[1, 0] = -1, 10_000_000
+        got, _ = run_attention(kalm, a, page_table=i32(table))
+        with pytest.raises(kalm.KalmError) as e:
+            kalm.kalm_check_device_errors()
+        assert e.value.name == "KALM_ERR_DEVICE_ARG"
+        codes = a["codes"].copy()
+        codes[row_index(a["table"], 16, 0, 32, 16)] = 0
+        codes[row_index(a["table"], 16, 1, 0, 16)] = 0
+        want, _, vmax = plain_attention(dict(a, codes=codes))
+        assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + 2.0 ** -15) * vmax[..., None]).all()
+    lq, nc = [40, 3], [70, 20]
+    q = torch.zeros(43, 6 * 256, dtype=torch.bfloat16, device="cuda")
+    c = torch.zeros(7 * 16, 512, dtype=torch.uint8, device="cuda")
+    s = torch.zeros(7 * 16, 16, dtype=torch.uint8, device="cuda")
+    out = torch.zeros(43, 1024, dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros(150, 512, dtype=torch.bfloat16, device="cuda")  # 90 + 2 * 64 rows are needed
+    kalm.kalm_merged_attention_cache(q[:, :1024], q[:, 1024:1280], q[:, 1280:], c[:, :256], s[:, :8], c[:, 256:], s[:, 8:],
+                                     i32([[0, 1, 2, 3, 4], [5, 6, 0, 0, 0]]), 16, i64([0, 40, 43]), i64([0, 70, 90]), 40, 4, 1,
+                                     out, workspace=ws)
+    with pytest.raises(kalm.KalmError) as e:
+        kalm.kalm_check_device_errors()
+    assert e.value.name == "KALM_ERR_DEVICE_ARG"
+
+
+def test_rows_that_are_not_32_byte_aligned(kalm):
+    """bf16 rows at 16-byte places (the other load and store width of write and read)."""
+    rng = np.random.default_rng(10)
+    v = rand_bf16(rng, (37, 96))
+    base = torch.zeros(37, 96 + 8, dtype=torch.bfloat16, device="cuda")
+    odd = base[:, 8:]   # 16 bytes past a 32-byte place, a stride of 208 bytes
+    odd.copy_(f64_to_dev(v))
+    codes, scales = torch.zeros(40, 96, dtype=torch.uint8, device="cuda"), torch.zeros(40, 3, dtype=torch.uint8, device="cuda")
+    table = i32([[4, 3, 2, 1, 0]])
+    kalm.kalm_cache_write(odd, i64([0, 37]), table, 8, codes, scales)
+    c, s = quantise(v)
+    at = row_index(np.array([[4, 3, 2, 1, 0]]), 8, 0, 0, 37)
+    np.testing.assert_array_equal(codes.cpu().numpy()[at], c)
+    np.testing.assert_array_equal(scales.cpu().numpy()[at], s)
+    back = torch.full((37, 104), 3.0, dtype=torch.bfloat16, device="cuda")
+    kalm.kalm_cache_read(codes, scales, i64([0, 37]), table, 8, back[:, 8:])
+    np.testing.assert_array_equal(from_dev(back)[:, 8:], dequantise(c, s))
+    assert (from_dev(back)[:, :8] == 3.0).all() and kalm.kalm_check_device_errors() == 0
+
+
+def test_captured_and_replayed_with_new_contents(kalm):
+    """Write, read and both forms of the attention in one graph, replayed after the inputs changed in place; two
+    graphs, each with its own scratch, replayed in turn."""
+    n_q, n_kv, d = 4, 1, 256
+    rng = np.random.default_rng(11)
+    lq, nc = [33, 33], [40, 70]
+    graphs = []
+    for k in range(2):
+        a = attention(rng, lq, nc, n_q, n_kv, 16)
+        r, n = sum(lq), a["codes"].shape[0]
+        st = dict(a=a, qkv=torch.empty(r, (n_q + 2 * n_kv) * d, dtype=torch.bfloat16, device="cuda"),
+                  src=torch.empty(sum(nc), 2 * d, dtype=torch.bfloat16, device="cuda"),
+                  back=torch.empty(sum(nc), 2 * d, dtype=torch.bfloat16, device="cuda"),
+                  codes=torch.zeros(n, 2 * d, dtype=torch.uint8, device="cuda"),
+                  scales=torch.zeros(n, 16, dtype=torch.uint8, device="cuda"),
+                  out=torch.empty(r, n_q * d, dtype=torch.bfloat16, device="cuda"),
+                  one=torch.empty(2, n_q * d, dtype=torch.bfloat16, device="cuda"), table=i32(a["table"]),
+                  q_off=i64(a["q_off"]), one_off=i64([0, 1, 2]), p_off=i64(a["p_off"]))
+
+        def step(s=st):
+            q, ks, vs = s["qkv"][:, :n_q * d], s["qkv"][:, n_q * d:n_q * d + d], s["qkv"][:, n_q * d + d:]
+            kalm.kalm_cache_write(s["src"], s["p_off"], s["table"], 16, s["codes"], s["scales"])
+            kalm.kalm_cache_read(s["codes"], s["scales"], s["p_off"], s["table"], 16, s["back"])
+            kv = (s["codes"][:, :d], s["scales"][:, :8], s["codes"][:, d:], s["scales"][:, 8:], s["table"], 16)
+            kalm.kalm_merged_attention_cache(q, ks, vs, *kv, s["q_off"], s["p_off"], 33, n_q, n_kv, s["out"])
+            kalm.kalm_merged_attention_cache(q[:2], ks[:2], vs[:2], *kv, s["one_off"], s["p_off"], 1, n_q, n_kv, s["one"])
+
+        step()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        graphs.append((g, st))
+    for round_ in range(3):
+        for g, s in graphs:
+            a = s["a"]
+            new = attention(rng, lq, nc, n_q, n_kv, 16)
+            a.update({k: new[k] for k in ("q", "ks", "vs")})
+            src = rand_bf16(rng, (sum(nc), 2 * d))
+            s["src"].copy_(f64_to_dev(src))
+            s["qkv"].copy_(torch.cat([f64_to_dev(a[k].reshape(sum(lq), -1)) for k in ("q", "ks", "vs")], 1))
+            s["out"].zero_(), s["one"].zero_(), s["back"].zero_()
+            c, sc = quantise(src)
+            for i in range(2):
+                at = cached_rows(a, i)
+                a["codes"][at], a["scales"][at] = c[a["p_off"][i]:a["p_off"][i + 1]], sc[a["p_off"][i]:a["p_off"][i + 1]]
+            g.replay()
+        torch.cuda.synchronize()
+        for g, s in graphs:
+            a = s["a"]
+            val = dequantise(a["codes"], a["scales"])
+            np.testing.assert_array_equal(from_dev(s["back"]), np.concatenate([val[cached_rows(a, i)] for i in range(2)]))
+            want, want_lse, vmax = plain_attention(a)
+            check(from_dev(s["out"]).reshape(want.shape), want_lse, want, want_lse, vmax)
+            one = dict(a, lq=[1, 1], q_off=np.array([0, 1, 2]), q=a["q"][:2], ks=a["ks"][:2], vs=a["vs"][:2])
+            want, want_lse, vmax = plain_attention(one)
+            check(from_dev(s["one"]).reshape(want.shape), want_lse, want, want_lse, vmax)
+    assert kalm.kalm_check_device_errors() == 0
+
+
+def test_two_streams_at_once(kalm):
+    """Calls on two side streams, each with its own scratch (the default one of either stream)."""
+    a = [attention(np.random.default_rng(20 + k), [130, 64], [256, 90], 4, 1, 64) for k in range(2)]
+    alone = [run_attention(kalm, x)[0] for x in a]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for k in range(2):
+            with torch.cuda.stream(streams[k]):
+                got, _ = run_attention(kalm, a[k], stream=streams[k])
+            np.testing.assert_array_equal(got, alone[k])
+    # both in flight, the arguments' streams given instead of entered
+    outs = []
+    n_q, d = 4, 256
+    for k in range(2):
+        x = a[k]
+        qkv = torch.cat([f64_to_dev(x[n].reshape(194, -1)) for n in ("q", "ks", "vs")], 1)
+        c, s = torch.from_numpy(x["codes"]).cuda(), torch.from_numpy(x["scales"]).cuda()
+        outs.append((qkv, c, s, i32(x["table"]), i64(x["q_off"]), i64(x["p_off"]),
+                     torch.empty(194, n_q * d, dtype=torch.bfloat16, device="cuda")))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for k in range(2):
+            qkv, c, s, table, q_off, p_off, out = outs[k]
+            kalm.kalm_merged_attention_cache(qkv[:, :1024], qkv[:, 1024:1280], qkv[:, 1280:], c[:, :256], s[:, :8], c[:, 256:],
+                                             s[:, 8:], table, 64, q_off, p_off, 130, 4, 1, out, stream=streams[k])
+    torch.cuda.synchronize()
+    for k in range(2):
+        np.testing.assert_array_equal(from_dev(outs[k][-1]).reshape(alone[k].shape), alone[k])
+
+
+def test_cache_offsets_past_32_bits(kalm):
+    """A cache of more than 4 GB: pages near its end are written, read and attended to at their own places."""
+    width, page_rows = 9216, 64
+    n_pages = (1 << 32) // (width * page_rows) + 40
+    free, _ = torch.cuda.mem_get_info()
+    if free < 8 << 30:
+        pytest.skip("needs 8 GB of device memory")
+    codes = torch.zeros(n_pages * page_rows, width, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(n_pages * page_rows, width // 32, dtype=torch.uint8, device="cuda")
+    rng = np.random.default_rng(12)
+    rows = [100, 3]
+    v = rand_bf16(rng, (103, width), 0.7)
+    table = np.array([[n_pages - 1, n_pages - 3], [n_pages - 2, -1]], np.int32)
+    off = i64([0, 100, 103])
+    kalm.kalm_cache_write(f64_to_dev(v), off, i32(table), page_rows, codes, scales)
+    c, s = quantise(v)
+    for d, (lo, hi) in enumerate(((0, 100), (100, 103))):
+        at = torch.from_numpy(row_index(table, page_rows, d, 0, hi - lo)).cuda()
+        np.testing.assert_array_equal(codes[at].cpu().numpy(), c[lo:hi])
+        np.testing.assert_array_equal(scales[at].cpu().numpy(), s[lo:hi])
+    assert int(codes[:(n_pages - 3) * page_rows].count_nonzero()) == 0
+    back = torch.empty(103, width, dtype=torch.bfloat16, device="cuda")
+    kalm.kalm_cache_read(codes, scales, off, i32(table), page_rows, back)
+    np.testing.assert_array_equal(from_dev(back), dequantise(c, s))
+    for lq in ([40, 2], [1, 1]):
+        k = 17 * 512  # the last layer's columns of 18
+        a = dict(lq=lq, nc=rows, n_q=4, n_kv=1, page_rows=128, q_off=offsets(lq), p_off=offsets(rows),
+                 table=np.array([[0], [1]]), codes=np.zeros((256, 512), np.uint8), scales=np.zeros((256, 16), np.uint8),
+                 q=rand_bf16(rng, (sum(lq), 4, 256), 0.7), ks=rand_bf16(rng, (sum(lq), 1, 256), 0.7),
+                 vs=rand_bf16(rng, (sum(lq), 1, 256)))
+        a["codes"][:100], a["codes"][128:131] = c[:100, k:], c[100:, k:]
+        a["scales"][:100], a["scales"][128:131] = s[:100, k // 32:], s[100:, k // 32:]
+        qkv = torch.cat([f64_to_dev(a[n].reshape(sum(lq), -1)) for n in ("q", "ks", "vs")], 1)
+        out = torch.empty(sum(lq), 1024, dtype=torch.bfloat16, device="cuda")
+        kalm.kalm_merged_attention_cache(qkv[:, :1024], qkv[:, 1024:1280], qkv[:, 1280:], codes[:, k:k + 256],
+                                         scales[:, k // 32:k // 32 + 8], codes[:, k + 256:], scales[:, k // 32 + 8:],
+                                         i32(table), page_rows, i64(a["q_off"]), off, max(lq), 4, 1, out)
+        want, want_lse, vmax = plain_attention(a)
+        check(from_dev(out).reshape(want.shape), want_lse, want, want_lse, vmax)
+    assert kalm.kalm_check_device_errors() == 0
+
+
+def test_repeated_calls_are_bit_identical(kalm):
+    a = attention(np.random.default_rng(13), [128] * 5 + [1], [256, 3, 0, 77, 128, 64], 4, 1, 16)
+    first = run_attention(kalm, a)
+    few = attention(np.random.default_rng(14), [1] * 40, list(range(20, 60)), 4, 1, 16)
+    few_first = run_attention(kalm, few)
+    for _ in range(5):
+        for x, y in ((a, first), (few, few_first)):
+            again = run_attention(kalm, x)
+            np.testing.assert_array_equal(again[0], y[0])
+            np.testing.assert_array_equal(again[1], y[1])
+
+
+def test_binding_refuses(kalm):
+    """What the Python calls check before the library does: types, shapes, strides, lengths."""
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8, device="cuda")
+    src, off, table = bf(20, 64), i64([0, 12, 20]), i32([[0, 1], [2, -1]])
+    codes, scales = u8(32, 64), u8(32, 2)
+    good = dict(src=src, row_off=off, page_table=table, page_rows=8, codes=codes, scales=scales)
+    kalm.kalm_cache_write(**good)
+    for bad in (dict(src=src.float()), dict(src=src[0]), dict(src=bf(64, 20).t()), dict(row_off=off.int()), dict(row_off=off[:0]),
+                dict(row_off=off[::2]), dict(page_table=table[:1]), dict(page_table=table.long()), dict(page_table=i32([0, 1])),
+                dict(page_table=i32([[0, 0, 0, 1], [2, 0, 0, 0]])[:, ::2]), dict(page_rows=7), dict(page_rows=0), dict(page_rows=-8),
+                dict(codes=codes[:, :32]), dict(codes=u8(32, 65)[:, :64]), dict(scales=scales[:16]), dict(scales=u8(32, 3)),
+                dict(codes=codes.view(torch.int8)), dict(first_row=i32([0])), dict(first_row=i64([0, 0])), dict(src=src.cpu()),
+                dict(codes=codes.cpu())):
+        with pytest.raises(kalm.KalmError) as e:
+            kalm.kalm_cache_write(**(good | bad))
+        assert e.value.name == "KALM_ERR_INVALID_ARG", bad
+    q, out = bf(6, 6 * 256), bf(6, 4 * 256)
+    kc, ks = u8(32, 512), u8(32, 16)
+    good = dict(q=q[:, :1024], k_self=q[:, 1024:1280], v_self=q[:, 1280:], k_codes=kc[:, :256], k_scales=ks[:, :8],
+                v_codes=kc[:, 256:], v_scales=ks[:, 8:], page_table=table, page_rows=8, q_off=i64([0, 3, 6]), pool_off=off,
+                max_q=3, n_q=4, n_kv=1, out=out)
+    kalm.kalm_merged_attention_cache(**good)
+    for bad in (dict(q=q), dict(v_self=q[:, 1280:].contiguous()), dict(v_codes=kc[:, 256:].contiguous()), dict(v_scales=ks[:, :16]),
+                dict(out=out[:, :768]), dict(q_off=i64([0, 6])), dict(q_off=i32([0, 3, 6])), dict(in_off=i64([0])),
+                dict(total_q=7), dict(lse=torch.zeros(6, 3, device="cuda")), dict(lse=torch.zeros(5, 4, device="cuda")),
+                dict(lse=torch.zeros(6, 4, device="cuda").half()), dict(order=i32([0])), dict(order=i64([0, 0, 0, 0])),
+                dict(workspace=bf(148, 256)), dict(workspace=bf(148, 1024)[:, :512]), dict(workspace=bf(148, 512).float()),
+                dict(max_q=513), dict(n_q=3), dict(scale=float("nan")), dict(scale=0.0), dict(head_dim=128), dict(n_kv=2),
+                dict(total_q=-1), dict(q=q[:, :1024].cpu())):
+        with pytest.raises(kalm.KalmError):
+            kalm.kalm_merged_attention_cache(**(good | bad))
+    assert kalm.kalm_check_device_errors() == 0

@@ -136,3 +136,46 @@ def test_a_row_of_nan_stays_a_row(kalm):
     h = torch.empty_like(clean)
     kalm.kalm_rms_norm(t, w, h)
     assert torch.isnan(h[2]).all() and torch.equal(h[[0, 1, 3]], clean[[0, 1, 3]])
+
+
+def test_captured_and_on_another_stream(kalm):
+    rng = np.random.default_rng(8)
+    y, x = f64_to_dev(rand_bf16(rng, (40, 640))), f64_to_dev(rand_bf16(rng, (40, 640)))
+    w, g = f64_to_dev(rand_bf16(rng, (640,))), f64_to_dev(rand_bf16(rng, (3, 640)))
+    off = i64([0, 10, 10, 40])
+    out, h = torch.empty_like(x), torch.empty_like(x)
+    call = lambda s=None: kalm.kalm_norm_residual(y, x, out, h=h, w_post=w, w_pre=w, gate=g, q_off=off, stream=s)
+    call()
+    want = out.clone(), h.clone()
+    side = torch.cuda.Stream()
+    out.zero_(), h.zero_()
+    torch.cuda.synchronize()
+    call(side)
+    side.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(h, want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    x.mul_(2), y.mul_(0.5)
+    graph.replay()
+    got = out.clone(), h.clone()
+    call()
+    assert torch.equal(out, got[0]) and torch.equal(h, got[1]) and not torch.equal(out, want[0])
+
+
+def test_binding_refuses(kalm):
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")
+    x, w = bf(4, 64), bf(64)
+    for bad in (dict(x=x.half()), dict(x=x[0]), dict(w=bf(63)), dict(w=w.float()), dict(h=bf(3, 64)), dict(h=bf(4, 72)),
+                dict(eps=0.0), dict(x=bf(64, 4).t()), dict(x=x.cpu()), dict(w=bf(128)[::2])):
+        with pytest.raises(kalm.KalmError):
+            kalm.kalm_rms_norm(**(dict(x=x, w=w, h=bf(4, 64)) | bad))
+    off = i64([0, 2, 4])
+    good = dict(y=bf(4, 64), x=x, x_out=bf(4, 64), h=bf(4, 64), w_post=w, w_pre=w, gate=bf(2, 64), q_off=off)
+    kalm.kalm_norm_residual(**good)
+    for bad in (dict(y=bf(5, 64)), dict(y=bf(4, 56)), dict(h=None), dict(w_pre=None), dict(q_off=None), dict(gate=bf(3, 64)),
+                dict(gate=bf(2, 72)), dict(gate=bf(63)), dict(q_off=off.int()), dict(q_off=off[:0]), dict(x_out=bf(3, 64)),
+                dict(h=good["x_out"]), dict(residual_scale=float("inf")), dict(w_post=bf(8)), dict(y=bf(4, 64).cpu())):
+        with pytest.raises(kalm.KalmError):
+            kalm.kalm_norm_residual(**(good | bad))
+    assert kalm.kalm_check_device_errors() == 0
