@@ -421,7 +421,10 @@ __device__ __forceinline__ void out_proj_phase(const AttnParams& p, const ProjPa
   }
 }
 
-template <bool FUSED>
+// FUSED: followed by the output projection.  CLEAN: what lies behind a document's last self row in its last self tile
+// (other documents' rows) is cleared in the V tile, so that a NaN or infinity there does not come through as
+// 0 * NaN; the softmax warps of such a tile do it while the tile's scores are the only thing they could wait for.
+template <bool FUSED, bool CLEAN>
 __global__ void __launch_bounds__(kThreads, 1)
     merged_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_ks,
                             const __grid_constant__ CUtensorMap tm_vs, const __grid_constant__ CUtensorMap tm_kc,
@@ -828,6 +831,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         l_own += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        if constexpr (CLEAN) {
+          const int own = it.Lq - j * kBKV;  // the document's rows in a self tile
+          if (j < it.n_self && own < kBKV) {
+            // (V_Jc landed; the next tile of this slot cannot: it waits for the product that waits for this warp)
+            const bool wv = mbar_wait(&bar_v[s], (Jc >> 1) & 1, p.wait_ns);
+            if (!__all_sync(0xffffffffu, wv)) {
+              ok = false;
+              break;
+            }
+            for (int u = own * 32 + r; u < kBKV * 32; u += kSoftmaxThreads / 2)  // 32 16-byte units a row, 8 a slab
+              *reinterpret_cast<uint4*>(sV + s * kKVBytes + ((u >> 3) & 3) * kKVSlab + (u >> 5) * 128 + (u & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
         fence_proxy_async_smem();
         if (__any_sync(0xffffffffu, rescale)) {
           // O must hold the result of PV_{Jc-1} before it is rescaled in place
@@ -1092,11 +1109,16 @@ __global__ void __launch_bounds__(kSchedThreads) attention_schedule_kernel(const
 
 kalm_status setup_attention_kernels() {
   kalm_status st = check_cuda(
-      cudaFuncSetAttribute(merged_attention_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
+      cudaFuncSetAttribute(merged_attention_kernel<false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kSmem),
       "cudaFuncSetAttribute(merged_attention_kernel)");
   if (st != KALM_OK) return st;
+  st = check_cuda(cudaFuncSetAttribute(merged_attention_kernel<false, true>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
+                  "cudaFuncSetAttribute(merged_attention_kernel<clean>)");
+  if (st != KALM_OK) return st;
   return check_cuda(
-      cudaFuncSetAttribute(merged_attention_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
+      cudaFuncSetAttribute(merged_attention_kernel<true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
       "cudaFuncSetAttribute(merged_attention_kernel<fused>)");
 }
 
@@ -1146,7 +1168,8 @@ kalm_status check_attention(const kalm_bf16* q, int64_t ldq, const kalm_bf16* k_
   return KALM_OK;
 }
 
-// `cross_pad`: rows between two documents' cross rows (0 where they are packed by pool_off).
+// `cross_pad`: rows between two documents' cross rows (0 where they are packed by pool_off); nonzero for the cache's
+// call, whose self V tiles are cleared behind a document's end.
 kalm_status launch_attention(const kalm_bf16* q, int64_t ldq, const kalm_bf16* k_self, const kalm_bf16* v_self,
                              int64_t ld_self, const kalm_bf16* k_cross, const kalm_bf16* v_cross, int64_t ld_cross,
                              const int64_t* q_off, const int64_t* in_off, int64_t total_in, const int64_t* pool_off,
@@ -1215,8 +1238,9 @@ kalm_status launch_attention(const kalm_bf16* q, int64_t ldq, const kalm_bf16* k
   const int sms = num_sms();
   const int64_t grid = items < sms ? items : sms;  // persistent: one CTA per SM
   if (!op) {
-    return check_cuda(launch_pdl(merged_attention_kernel<false>, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
-                                 kSmem, static_cast<cudaStream_t>(stream), tq, tks, tvs, tkc, tvc, tq, tq, prm,
+    return check_cuda(launch_pdl(cross_pad ? merged_attention_kernel<false, true> : merged_attention_kernel<false, false>,
+                                 dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmem,
+                                 static_cast<cudaStream_t>(stream), tq, tks, tvs, tkc, tvc, tq, tq, prm,
                                  ProjParams{}),
                       "launch merged_attention_kernel");
   }
@@ -1245,7 +1269,7 @@ kalm_status launch_attention(const kalm_bf16* q, int64_t ldq, const kalm_bf16* k
   if (otiles + grid > INT32_MAX) return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention_out_proj: too many tiles");
   fp.n_otiles = static_cast<int>(otiles);
   fp.sync = op->sync;
-  return check_cuda(launch_pdl(merged_attention_kernel<true>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmem,
+  return check_cuda(launch_pdl(merged_attention_kernel<true, false>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmem,
                                static_cast<cudaStream_t>(stream), tq, tks, tvs, tkc, tvc, toa, two, prm, fp),
                     "launch merged_attention_kernel<fused>");
 }

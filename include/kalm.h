@@ -539,10 +539,11 @@ kalm_status kalm_cache_read(const uint8_t* codes, int64_t ld_codes, const uint8_
  *          document that reaches past it is flagged); scratch, no contents are
  *          kept from call to call.  Calls that overlap on the GPU need their own.
  *          NULL with 0 rows where ld_table is 0 (nothing cached) or the rows are few.
- * What lies behind a document's last cached row has no influence, NaN and
- * infinities included.  As with kalm_merged_attention, the self rows are to be
- * finite: a NaN or infinity in a V row reaches the query tiles (128 / (n_q / n_kv)
- * positions) that load its 64-row tile, those of the document before included. */
+ * Other documents' rows, self or cached, and what lies behind a document's last
+ * row have no influence, NaN and infinities included.  Within a document, a NaN or
+ * infinity in a self V row can also reach the decoder rows before it (the mask
+ * makes its probability zero, and 0 * NaN is NaN).
+ * At most 65,535 documents a call. */
 kalm_status kalm_merged_attention_cache(const kalm_bf16* q, int64_t ldq, const kalm_bf16* k_self,
                                         const kalm_bf16* v_self, int64_t ld_self, const uint8_t* k_codes,
                                         const uint8_t* v_codes, int64_t ld_codes, const uint8_t* k_scales,

@@ -667,3 +667,24 @@ def test_binding_refuses(kalm):
         with pytest.raises(kalm.KalmError):
             kalm.kalm_merged_attention_cache(**(good | bad))
     assert kalm.kalm_check_device_errors() == 0
+
+
+@pytest.mark.parametrize("lq", [[5, 40, 64, 1, 130], [1, 1, 1, 1, 1], [70, 63, 65, 2, 17]])
+def test_one_documents_nan_stays_its_own(kalm, lq):
+    """NaN and infinities in every self row and cached row of some documents leave the others' results, bit for bit."""
+    rng = np.random.default_rng(sum(lq))
+    a = attention(rng, lq, [30, 7, 65, 0, 100], 4, 1, 16)
+    clean, clean_lse = run_attention(kalm, a)
+    b = dict(a, **{k: a[k].copy() for k in ("q", "ks", "vs", "codes")})
+    for d, x in ((1, np.nan), (3, np.inf), (4, -np.inf)):
+        rows = slice(a["q_off"][d], a["q_off"][d + 1])
+        b["ks"][rows], b["vs"][rows] = x, x
+        b["q"][rows] = np.nan
+        b["codes"][cached_rows(a, d)] = 0x7F
+    got, lse = run_attention(kalm, b, poison=True)
+    for d in (0, 2):
+        rows = slice(a["q_off"][d], a["q_off"][d + 1])
+        np.testing.assert_array_equal(got[rows], clean[rows])
+        np.testing.assert_array_equal(lse[rows], clean_lse[rows])
+    assert np.isfinite(clean).all() and not np.isfinite(got[a["q_off"][1]]).any()
+    assert kalm.kalm_check_device_errors() == 0
