@@ -423,7 +423,8 @@ __device__ __forceinline__ void out_proj_phase(const AttnParams& p, const ProjPa
 
 // FUSED: followed by the output projection.  CLEAN: what lies behind a document's last self row in its last self tile
 // (other documents' rows) is cleared in the V tile, so that a NaN or infinity there does not come through as
-// 0 * NaN; the softmax warps of such a tile do it while the tile's scores are the only thing they could wait for.
+// 0 * NaN; the warp that issues the P V products does it, with all its lanes (in the softmax warps, whose registers
+// are all taken, the same cost 4% of a layer whose documents have no such tile).
 template <bool FUSED, bool CLEAN>
 __global__ void __launch_bounds__(kThreads, 1)
     merged_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_ks,
@@ -677,37 +678,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMmaWarpPV) {
     // ------------------------------------------------------------ P V issuer
-    if (lane == 0) {
+    // (CLEAN: every lane walks along and helps to clear, lane 0 issues; their votes keep the warp together)
+    if (CLEAN || lane == 0) {
       const uint32_t v_base = smem_u32(sV), p_base = smem_u32(sP);
       uint32_t J = 0;
       int n_it = 0;
       bool ok = true;
       int64_t last_j = -1;  // last P V issued (for the drain)
+      auto agreed = [&](bool good) { return CLEAN ? __all_sync(0xffffffffu, good) != 0 : good; };
       int wc = item_at(p, 0);
       Item nxt = load_item(p, wc);
-      for (int pass = 0; wc != kNoMore && ok && !*abort_flag; ++pass) {
+      for (int pass = 0; wc != kNoMore && ok && agreed(!*abort_flag); ++pass) {
         const Item it = nxt;
         wc = item_at(p, pass + 1);
         nxt = load_item(p, wc);
         if (it.nt == 0) continue;
-        for (int j = 0; j < it.nt && ok && !*abort_flag; ++j) {
+        for (int j = 0; j < it.nt && ok && agreed(!*abort_flag); ++j) {
           const uint32_t Jc = J + j;
           const int s = Jc & 1;
-          if (!mbar_wait(&bar_p[s], (Jc >> 1) & 1, p.wait_ns) ||
-              !mbar_wait(&bar_v[s], (Jc >> 1) & 1, p.wait_ns) ||
-              (j == 0 && n_it >= 1 && !mbar_wait(bar_ofree, (n_it - 1) & 1, p.wait_ns))) {
+          if (!agreed(mbar_wait(&bar_p[s], (Jc >> 1) & 1, p.wait_ns) &&
+                      mbar_wait(&bar_v[s], (Jc >> 1) & 1, p.wait_ns) &&
+                      (j != 0 || n_it < 1 || mbar_wait(bar_ofree, (n_it - 1) & 1, p.wait_ns)))) {
             ok = false;
             break;
           }
           tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < kBKV / 16; ++kk) {
-            const uint64_t ad = sdesc_sw128(p_base + s * kPBytes + kk * 32, 16, 1024);
-            // V is MN-major: 64-column slabs kKVSlab apart (LBO), 8-key groups 1024 B apart (SBO)
-            const uint64_t bd = sdesc_sw128(v_base + s * kKVBytes + kk * 16 * 128, kKVSlab, 1024);
-            umma_bf16_ss(tmem, ad, bd, kIdescPV, (j | kk) != 0 ? 1u : 0u);
+          if constexpr (CLEAN) {
+            const int own = it.Lq - j * kBKV;  // the document's rows in a self tile
+            if (j < it.n_self && own < kBKV) {
+              for (int u = own * 32 + lane; u < kBKV * 32; u += 32)  // 32 16-byte units a row, 8 a 64-column slab
+                *reinterpret_cast<uint4*>(sV + s * kKVBytes + ((u >> 3) & 3) * kKVSlab + (u >> 5) * 128 +
+                                          (u & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+              fence_proxy_async_smem();
+            }
+            __syncwarp();
           }
-          umma_commit(&bar_pv[s]);
+          if (!CLEAN || lane == 0) {
+#pragma unroll
+            for (int kk = 0; kk < kBKV / 16; ++kk) {
+              const uint64_t ad = sdesc_sw128(p_base + s * kPBytes + kk * 32, 16, 1024);
+              // V is MN-major: 64-column slabs kKVSlab apart (LBO), 8-key groups 1024 B apart (SBO)
+              const uint64_t bd = sdesc_sw128(v_base + s * kKVBytes + kk * 16 * 128, kKVSlab, 1024);
+              umma_bf16_ss(tmem, ad, bd, kIdescPV, (j | kk) != 0 ? 1u : 0u);
+            }
+            umma_commit(&bar_pv[s]);
+          }
           last_j = Jc;
         }
         J += it.nt;
@@ -831,20 +846,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         l_own += (acc[0] + acc[1]) + (acc[2] + acc[3]);
-        if constexpr (CLEAN) {
-          const int own = it.Lq - j * kBKV;  // the document's rows in a self tile
-          if (j < it.n_self && own < kBKV) {
-            // (V_Jc landed; the next tile of this slot cannot: it waits for the product that waits for this warp)
-            const bool wv = mbar_wait(&bar_v[s], (Jc >> 1) & 1, p.wait_ns);
-            if (!__all_sync(0xffffffffu, wv)) {
-              ok = false;
-              break;
-            }
-            for (int u = own * 32 + r; u < kBKV * 32; u += kSoftmaxThreads / 2)  // 32 16-byte units a row, 8 a slab
-              *reinterpret_cast<uint4*>(sV + s * kKVBytes + ((u >> 3) & 3) * kKVSlab + (u >> 5) * 128 + (u & 7) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
-          }
-        }
         fence_proxy_async_smem();
         if (__any_sync(0xffffffffu, rescale)) {
           // O must hold the result of PV_{Jc-1} before it is rescaled in place
