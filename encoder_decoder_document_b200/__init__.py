@@ -395,6 +395,7 @@ def kalm_merged_attention_cache(q: torch.Tensor, k_self: torch.Tensor, v_self: t
     CACHE_FEW_ROWS packed rows a KV head (max_q * n_q / n_kv) use none."""
     where = "kalm_merged_attention_cache"
     bf16 = torch.bfloat16
+    max_q, page_rows = int(max_q), int(page_rows)
     dev = _device(where, q)
     width, rows = n_kv * head_dim, q.shape[0]
     n_docs, ld_table, n_pages, ld_codes, ld_scales = _cache_args(where, dev, pool_off, page_table, page_rows, k_codes,
@@ -405,8 +406,7 @@ def kalm_merged_attention_cache(q: torch.Tensor, k_self: torch.Tensor, v_self: t
     _pair(where, "scales", k_scales, v_scales)
     ldq = _mat(where, "q", q, bf16, dev, rows, n_q * head_dim)
     ldo = _mat(where, "out", out, bf16, dev, -1, n_q * head_dim)
-    if total_q is None:
-        total_q = out.shape[0]
+    total_q = out.shape[0] if total_q is None else int(total_q)
     if total_q > out.shape[0] or (in_off is None and total_q > rows):
         raise KalmError(1, where, f"total_q={total_q} exceeds the rows of out ({out.shape[0]}) or q ({rows})")
     if lse is not None and (lse.dtype is not torch.float32 or lse.get_device() != dev or lse.dim() != 2 or
@@ -434,7 +434,7 @@ def kalm_merged_attention_cache(q: torch.Tensor, k_self: torch.Tensor, v_self: t
          v_codes.data_ptr(), ld_codes, k_scales.data_ptr(), v_scales.data_ptr(), ld_scales, page_table.data_ptr(),
          ld_table, page_rows, n_pages, _vec(where, "q_off", q_off, torch.int64, dev, n_docs + 1),
          _vec(where, "in_off", in_off, torch.int64, dev, n_docs), rows, pool_off.data_ptr(), n_docs, max_q, total_q,
-         n_q, n_kv, head_dim, head_dim ** -0.5 if scale is None else scale, 1 if last_tile_only else 0,
+         n_q, n_kv, head_dim, head_dim ** -0.5 if scale is None else float(scale), 1 if last_tile_only else 0,
          None if order is None else order.data_ptr(), ws, ws_rows, out.data_ptr(), ldo,
          None if lse is None else lse.data_ptr(), _stream(stream))
 
@@ -452,7 +452,8 @@ def kalm_rms_norm(x: torch.Tensor, w: torch.Tensor, h: torch.Tensor, eps: float 
     ldx = _mat(where, "x", x, torch.bfloat16, dev)
     rows, width = x.shape
     call(where, x.data_ptr(), ldx, _vec(where, "w", w, torch.bfloat16, dev, width), h.data_ptr(),
-         _mat(where, "h", h, torch.bfloat16, dev, rows, width), rows, width, eps, weight_offset, _stream(stream))
+         _mat(where, "h", h, torch.bfloat16, dev, rows, width), rows, width, float(eps), float(weight_offset),
+         _stream(stream))
 
 
 def kalm_norm_residual(y: torch.Tensor, x: torch.Tensor, x_out: torch.Tensor, h: Optional[torch.Tensor] = None,
@@ -482,10 +483,10 @@ def kalm_norm_residual(y: torch.Tensor, x: torch.Tensor, x_out: torch.Tensor, h:
         gate_at = _vec(where, "gate", gate, bf16, dev, width)
     call(where, y.data_ptr(), _mat(where, "y", y, bf16, dev, rows, width), x.data_ptr(), ldx,
          _vec(where, "w_post", w_post, bf16, dev, width), gate_at, ld_gate,
-         _vec(where, "q_off", q_off, torch.int64, dev, n_docs + 1), n_docs, residual_scale, x_out.data_ptr(),
+         _vec(where, "q_off", q_off, torch.int64, dev, n_docs + 1), n_docs, float(residual_scale), x_out.data_ptr(),
          _mat(where, "x_out", x_out, bf16, dev, rows, width), _vec(where, "w_pre", w_pre, bf16, dev, width),
          None if h is None else h.data_ptr(), 0 if h is None else _mat(where, "h", h, bf16, dev, rows, width), rows,
-         width, eps, weight_offset, _stream(stream))
+         width, float(eps), float(weight_offset), _stream(stream))
 
 
 def kalm_selftest_wait_timeout(wait_ns: int, stream=None) -> None:

@@ -3,8 +3,8 @@
 //
 // A cached row holds e4m3 codes and, for each 32 consecutive columns, one scale byte b that stands for
 // 2^(b - 127).  kalm_cache_write keeps b in [7, 247], so that every stored value code * 2^(b - 127) is a bf16
-// number: the codes are multiples of 2^-9, and 2^-9 * 2^-120 is above bf16's least subnormal 2^-133; the largest,
-// 448 * 2^119 = 240 * 2^120 * 0.933.., lies below 2^128.
+// number: a code has four significant bits and is a multiple of 2^-9, and 2^-9 * 2^-120 is a multiple of bf16's
+// least subnormal 2^-133; the largest, 240 * 2^120 and 448 * 2^119, lie below 2^128.
 #pragma once
 
 #include <cstdint>
@@ -14,9 +14,11 @@
 
 #include "kalm.h"
 #include "kalm_ptx.cuh"
+#include "kalm_wide.cuh"
 
 namespace kalm {
 
+constexpr uint32_t kSiteCache = 8u << 8;  // device error word (see kalm_check_device_errors in kalm.h)
 constexpr int kCacheGroup = KALM_CACHE_GROUP;  // columns that share a scale
 constexpr int kCacheMinExp = -120;  // least scale exponent
 constexpr int kCacheMaxExp = 120;   // greatest: bf16's largest value needs it

@@ -1297,16 +1297,17 @@ extern "C" kalm_status kalm_merged_attention(const kalm_bf16* q, int64_t ldq, co
 //
 // Widening inside the attention kernel was built and measured: eight more warps wrote each tile from its codes to
 // shared memory, no workspace.  A layer of 100 documents x 128 positions (4 query tiles a document, so every
-// cached tile is widened 4 times) took 55 us against 38 us for the two launches, 100 documents x 256 positions
-// of 8 heads 157 us against 116 us, one position per document 19 us against 15 us: a tile's widening takes
-// about 3,500 cycles of a warp pair on the schedulers that the softmax also needs, more than the 1,700
-// cycles in which the bf16 kernel consumes a tile.
+// cached tile is widened 4 times) took 55 us against 41.5 us for the two launches (31.6 us of them the attention),
+// 100 documents x 256 positions of 8 heads 157 us against 120 us (105 us), one position per document 19 us against
+// 20 us: a tile's widening takes about 3,500 cycles of a warp pair on the schedulers that the softmax also
+// needs, more than the 1,700 cycles in which the bf16 kernel consumes a tile.
 //
 // Widening kernel: a block takes some rows of a document, all heads of K and V: a warp a row at a time, sixteen
 // lanes a head vector (16 codes each), so that its loads are whole lines of the cached row and its stores 1 KB
 // runs.  Rows up to the next multiple of 64 become zeros, so that the attention's last tile of a document multiplies
 // its masked probabilities with finite values.  Bound by latency at these sizes (two dependent loads: the
-// document's offsets and pages, then the codes); 3 + 1/32 bytes a value.
+// document's offsets and pages, then the codes; 20 MB at the Nano shape in about 6 us beside the attention);
+// 3 + 1/32 bytes a value.
 namespace kalm {
 namespace {
 
@@ -1333,9 +1334,10 @@ __global__ void __launch_bounds__(kWidenThreads) cache_widen_kernel(const WidenP
   pdl_wait_predecessor();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int d = blockIdx.y;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kWidenWarps * p.warp_rows + warp * p.warp_rows;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kWidenWarps * p.warp_rows;
+  int64_t r0 = (static_cast<int64_t>(blockIdx.x) * kWidenWarps + warp) * p.warp_rows;
   // lane l < warp_rows looks up row r0 + l; the page is asked for beside the offsets, before its row is known to exist
-  const int32_t page = lane < p.warp_rows ? cache_page(p.pages, d, r0 + lane) : -1;
+  int32_t page = lane < p.warp_rows ? cache_page(p.pages, d, r0 + lane) : -1;
   const int64_t c0 = __ldg(p.pool_off + d);
   const int64_t nc = __ldg(p.pool_off + d + 1) - c0;
   const int64_t end = (nc + kBKV - 1) / kBKV * kBKV;            // rows that the attention's tiles touch
@@ -1345,41 +1347,47 @@ __global__ void __launch_bounds__(kWidenThreads) cache_widen_kernel(const WidenP
     if (lane == 0) record_error(p.err, kErrDeviceArg | kSiteAttention);
     return;
   }
-  int64_t mine = -1;
-  if (lane < p.warp_rows && r0 + lane < nc) {
-    mine = cache_row(p.pages, page, r0 + lane);
-    if (mine < 0) record_error(p.err, kErrDeviceArg | kSiteAttention);
-  }
-  // step q of the warp: row q / n_kv, the head vectors 2 (q % n_kv) and the one after it of [K heads, V heads]
-  const int steps = static_cast<int>(min(static_cast<int64_t>(p.warp_rows), end - r0)) * p.n_kv, c = lane & 15;
   const uint8_t *const k_codes = p.codes[0], *const v_codes = p.codes[1];
   const uint8_t *const k_scales = p.scales[0], *const v_scales = p.scales[1];
-  __nv_bfloat16* const dst = p.ws + (to + r0) * p.n_kv * (2 * kD) + lane * 16;
-  int row = 0, vec = lane >> 4;
-  for (int q0 = 0; q0 < steps; q0 += kWidenAhead) {
-    uint4 x[kWidenAhead];
-    uint32_t s[kWidenAhead];
-#pragma unroll
-    for (int i = 0; i < kWidenAhead; ++i) {
-      const int64_t at = __shfl_sync(0xffffffffu, mine, row & 31);
-      x[i] = make_uint4(0u, 0u, 0u, 0u);
-      s[i] = 0;
-      if (q0 + i < steps && at >= 0) {
-        const bool v = vec >= p.n_kv;
-        const int g = v ? vec - p.n_kv : vec;
-        x[i] = __ldg(reinterpret_cast<const uint4*>((v ? v_codes : k_codes) + at * p.ld_codes + g * kD) + c);
-        s[i] = __ldg((v ? v_scales : k_scales) + at * p.ld_scales + g * (kD / kCacheGroup) + (c >> 1));
-      }
-      vec += 2;
-      if (vec >= 2 * p.n_kv) {
-        vec = lane >> 4;
-        ++row;
-      }
+  while (true) {
+    int64_t mine = -1;
+    if (lane < p.warp_rows && r0 + lane < nc) {
+      mine = cache_row(p.pages, page, r0 + lane);
+      if (mine < 0) record_error(p.err, kErrDeviceArg | kSiteAttention);
     }
+    // step q of the warp: row q / n_kv, the head vectors 2 (q % n_kv) and the one after it of [K heads, V heads]
+    const int steps = static_cast<int>(min(static_cast<int64_t>(p.warp_rows), end - r0)) * p.n_kv, c = lane & 15;
+    __nv_bfloat16* const dst = p.ws + (to + r0) * p.n_kv * (2 * kD) + lane * 16;
+    int row = 0, vec = lane >> 4;
+    for (int q0 = 0; q0 < steps; q0 += kWidenAhead) {
+      uint4 x[kWidenAhead];
+      uint32_t s[kWidenAhead];
 #pragma unroll
-    for (int i = 0; i < kWidenAhead; ++i)
-      if (q0 + i < steps)
-        stg_words8(dst + static_cast<int64_t>(q0 + i) * (2 * kD), e4m3x16_scaled(x[i], scale_bf16x2(s[i])));
+      for (int i = 0; i < kWidenAhead; ++i) {
+        const int64_t at = __shfl_sync(0xffffffffu, mine, row & 31);
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
+        s[i] = 0;
+        if (q0 + i < steps && at >= 0) {
+          const bool v = vec >= p.n_kv;
+          const int g = v ? vec - p.n_kv : vec;
+          x[i] = __ldg(reinterpret_cast<const uint4*>((v ? v_codes : k_codes) + at * p.ld_codes + g * kD) + c);
+          s[i] = __ldg((v ? v_scales : k_scales) + at * p.ld_scales + g * (kD / kCacheGroup) + (c >> 1));
+        }
+        vec += 2;
+        if (vec >= 2 * p.n_kv) {
+          vec = lane >> 4;
+          ++row;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kWidenAhead; ++i)
+        if (q0 + i < steps)
+          stg_words8(dst + static_cast<int64_t>(q0 + i) * (2 * kD), e4m3x16_scaled(x[i], scale_bf16x2(s[i])));
+    }
+    // the grid covers what the table has places for; a document that claims more gets zeros there, flagged
+    r0 += stride;
+    if (r0 >= end) return;
+    page = lane < p.warp_rows ? cache_page(p.pages, d, r0 + lane) : -1;
   }
 }
 
@@ -1403,7 +1411,7 @@ extern "C" kalm_status kalm_merged_attention_cache(
   // few packed rows a KV head: no tensor-core tiles, no workspace
   const bool few = n_kv > 0 && n_q > 0 && n_q % n_kv == 0 && max_q >= 0 &&
                    static_cast<int64_t>(max_q) * (n_q / n_kv) <= KALM_CACHE_FEW_ROWS;
-  const int64_t rows = ld_table > 0 && !few ? workspace_rows : 0;  // no pages: nothing cached
+  const int64_t rows = few ? 0 : workspace_rows;
   kalm_status st = check_attention(q, ldq, k_self, v_self, ld_self, workspace, workspace, 2 * width, q_off, in_off,
                                    total_in, pool_off, n_docs, max_q, total_q, rows, n_q, n_kv, head_dim, scale, out,
                                    ldo);
@@ -1428,8 +1436,9 @@ extern "C" kalm_status kalm_merged_attention_cache(
                   "kalm_merged_attention_cache: codes must be 16-byte aligned, the strides (%lld, a multiple of 16; "
                   "%lld) cover all heads",
                   (long long)ld_codes, (long long)ld_scales);
-    if (n_docs > 65535) return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention_cache: n_docs=%d", n_docs);
   }
+  if (any && !few && n_docs > 65535)
+    return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention_cache: n_docs=%d (at most 65,535)", n_docs);
   if ((st = ensure_device(nullptr)) != KALM_OK) return st;
   if (any && few) {
     CacheRowsParams p{};
@@ -1460,17 +1469,17 @@ extern "C" kalm_status kalm_merged_attention_cache(
     p.err = device_error_word();
     return launch_cache_rows_attention(p, n_docs, static_cast<cudaStream_t>(stream));
   }
-  if (any && ld_table > 0) {
+  if (any) {
     const int warp_rows = n_kv >= kWidenAhead ? 1 : kWidenAhead / n_kv;
     const int64_t rows_max = (ld_table * page_rows + kBKV - 1) / kBKV * kBKV;  // of a document, with its zeros
-    const int block_rows = kWidenWarps * warp_rows;
+    const int64_t block_rows = kWidenWarps * warp_rows;
+    const int64_t blocks = rows_max > block_rows ? (rows_max + block_rows - 1) / block_rows : 1;
     const WidenParams wp{{k_codes, v_codes}, {k_scales, v_scales}, ld_codes, ld_scales,
                          CachePages{page_table, ld_table, n_pages, __builtin_ctz(static_cast<unsigned>(page_rows))},
-                         pool_off, reinterpret_cast<__nv_bfloat16*>(workspace), workspace_rows, n_kv,
+                         pool_off, reinterpret_cast<__nv_bfloat16*>(workspace), rows, n_kv,
                          warp_rows, device_error_word()};
     st = check_cuda(launch_pdl(cache_widen_kernel,
-                               dim3(static_cast<unsigned>((rows_max + block_rows - 1) / block_rows),
-                                    static_cast<unsigned>(n_docs)),
+                               dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(n_docs)),
                                dim3(kWidenThreads), 0, static_cast<cudaStream_t>(stream), wp),
                     "launch cache_widen_kernel");
     if (st != KALM_OK) return st;

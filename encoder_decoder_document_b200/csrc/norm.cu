@@ -20,6 +20,7 @@
 #include "kalm.h"
 #include "kalm_internal.h"
 #include "kalm_ptx.cuh"
+#include "kalm_wide.cuh"
 
 namespace kalm {
 namespace {

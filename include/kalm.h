@@ -543,7 +543,7 @@ kalm_status kalm_cache_read(const uint8_t* codes, int64_t ld_codes, const uint8_
  * row have no influence, NaN and infinities included.  Within a document, a NaN or
  * infinity in a self V row can also reach the decoder rows before it (the mask
  * makes its probability zero, and 0 * NaN is NaN).
- * At most 65,535 documents a call. */
+ * At most 65,535 documents a call of more than few rows. */
 kalm_status kalm_merged_attention_cache(const kalm_bf16* q, int64_t ldq, const kalm_bf16* k_self,
                                         const kalm_bf16* v_self, int64_t ld_self, const uint8_t* k_codes,
                                         const uint8_t* v_codes, int64_t ld_codes, const uint8_t* k_scales,

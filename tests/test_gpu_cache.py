@@ -293,7 +293,7 @@ def plain_attention(a, scale=1 / 16, in_off=None):
 
 
 def run_attention(kalm, a, scale=1 / 16, order=None, in_off=None, last=False, poison=False, stream=None, page_table=None,
-                  max_q=None):
+                  max_q=None, ws_rows=None):
     d, n_q, n_kv = 256, a["n_q"], a["n_kv"]
     rows = a["q"].shape[0]
     q_off, p_off = i64(a["q_off"]), i64(a["p_off"])
@@ -319,7 +319,8 @@ def run_attention(kalm, a, scale=1 / 16, order=None, in_off=None, last=False, po
         i32(a["table"]) if page_table is None else page_table, a["page_rows"], q_off, p_off, max_q or max(a["lq"]),
         n_q, n_kv, out,
         scale, lse, in_off=None if in_off is None else i64(in_off), last_tile_only=last,
-        order=order(q_off, p_off) if order else None, stream=stream)
+        order=order(q_off, p_off) if order else None, stream=stream,
+        workspace=None if ws_rows is None else torch.full((ws_rows, 2 * w), float("nan"), dtype=torch.bfloat16, device="cuda"))
     if stream is not None:
         stream.synchronize()
     return from_dev(out).reshape(r, n_q, d), lse.cpu().numpy().astype(np.float64)
@@ -688,3 +689,26 @@ def test_one_documents_nan_stays_its_own(kalm, lq):
         np.testing.assert_array_equal(lse[rows], clean_lse[rows])
     assert np.isfinite(clean).all() and not np.isfinite(got[a["q_off"][1]]).any()
     assert kalm.kalm_check_device_errors() == 0
+
+
+@pytest.mark.parametrize("lq,page_rows,places", [([40, 3], 16, 2), ([40, 3], 8, 1), ([40, 3], 8, 0), ([1, 1], 16, 2), ([1, 1], 8, 0)])
+def test_attention_rows_past_the_table(kalm, lq, page_rows, places):
+    """Documents that claim more rows than their table has places for: the rest count as zeros and are flagged."""
+    nc = [200, 70]
+    a = attention(np.random.default_rng(15), lq, nc, 4, 1, page_rows)
+    codes = np.zeros_like(a["codes"])
+    for d in range(2):
+        at = cached_rows(a, d)[:places * page_rows]
+        codes[at] = a["codes"][at]
+    got, lse = run_attention(kalm, a, page_table=i32(a["table"][:, :places].copy()), ws_rows=270 + 2 * 64)
+    with pytest.raises(kalm.KalmError) as e:
+        kalm.kalm_check_device_errors()
+    assert e.value.name == "KALM_ERR_DEVICE_ARG"
+    check(got, lse, *plain_attention(dict(a, codes=codes)))
+
+
+def test_numpy_numbers_as_sizes(kalm):
+    a = attention(np.random.default_rng(16), [3, 20], [9, 30], 4, 1, 8)
+    got, _ = run_attention(kalm, a, scale=np.float32(1 / 16), max_q=np.int64(20))
+    want, _ = run_attention(kalm, a)
+    np.testing.assert_array_equal(got, want)
