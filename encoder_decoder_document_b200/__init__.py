@@ -32,11 +32,17 @@ CACHE_GROUP = 32  # KALM_CACHE_GROUP: columns of a cached row that share a scale
 CACHE_FEW_ROWS = 4  # KALM_CACHE_FEW_ROWS: packed rows up to which the cache attention takes no workspace
 
 
-def _stream(stream: Optional[torch.cuda.Stream]) -> int:
+# The current device and a device's current stream handle as torch keeps them, without the checks and the Stream
+# object around them (0.1 us instead of 3 us a call); called with a CUDA tensor in hand, so CUDA is initialised.
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream: Optional[torch.cuda.Stream], dev: Optional[int] = None) -> int:
+    """Handle of a stream, or of the current one of `dev` (None: the current device)."""
     if stream is not None:
         return stream.cuda_stream
-    # the current stream's handle without the Stream object around it (0.1 us instead of 3 us a call)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return _current_stream(torch.cuda.current_device() if dev is None else dev)
 
 
 def _p(t: Optional[torch.Tensor], dtype: Optional[torch.dtype] = None) -> Optional[int]:
@@ -69,7 +75,7 @@ def _device(where: str, t: torch.Tensor) -> int:
     """The current device, on which the call's tensors must live."""
     if not t.is_cuda:
         raise KalmError(1, where, "tensors must live on the CUDA device")
-    return torch.cuda.current_device()
+    return _current_device()
 
 
 def _mat(where: str, name: str, t: torch.Tensor, dtype: torch.dtype, dev: int, rows: int = -1, width: int = -1) -> int:
@@ -359,7 +365,7 @@ def kalm_cache_write(src: torch.Tensor, row_off: torch.Tensor, page_table: torch
                                                                  scales, width)
     call(where, src.data_ptr(), ld_src, row_off.data_ptr(), n_docs, rows, width,
          _vec(where, "first_row", first_row, torch.int32, dev, n_docs), page_table.data_ptr(), ld_table, page_rows,
-         n_pages, codes.data_ptr(), ld_codes, scales.data_ptr(), ld_scales, _stream(stream))
+         n_pages, codes.data_ptr(), ld_codes, scales.data_ptr(), ld_scales, _stream(stream, dev))
 
 
 def kalm_cache_read(codes: torch.Tensor, scales: torch.Tensor, row_off: torch.Tensor, page_table: torch.Tensor,
@@ -374,7 +380,7 @@ def kalm_cache_read(codes: torch.Tensor, scales: torch.Tensor, row_off: torch.Te
                                                                  scales, width)
     call(where, codes.data_ptr(), ld_codes, scales.data_ptr(), ld_scales, row_off.data_ptr(), n_docs, rows, width,
          _vec(where, "first_row", first_row, torch.int32, dev, n_docs), page_table.data_ptr(), ld_table, page_rows,
-         n_pages, dst.data_ptr(), ld_dst, _stream(stream))
+         n_pages, dst.data_ptr(), ld_dst, _stream(stream, dev))
 
 
 def kalm_merged_attention_cache(q: torch.Tensor, k_self: torch.Tensor, v_self: torch.Tensor, k_codes: torch.Tensor,
@@ -413,7 +419,7 @@ def kalm_merged_attention_cache(q: torch.Tensor, k_self: torch.Tensor, v_self: t
                             lse.shape[0] < total_q or lse.shape[1] != n_q or not lse.is_contiguous()):
         _refuse(where, "lse", lse, torch.float32, dev, f"expected a contiguous [{total_q}][{n_q}] tensor")
     if order is not None:
-        tile = max(128 * n_kv // n_q, 1) if n_q > 0 else 1  # positions of a query tile, as kalm_attention_items counts them
+        tile = max(128 * n_kv // n_q, 1) if n_q > 0 else 1  # positions of a query tile, as in kalm_attention_items
         items = n_docs * n_kv * (1 if last_tile_only else -(-max_q // tile))
         if order.dtype is not torch.int32 or order.get_device() != dev or order.numel() < items or \
                 not order.is_contiguous():
@@ -436,7 +442,7 @@ def kalm_merged_attention_cache(q: torch.Tensor, k_self: torch.Tensor, v_self: t
          _vec(where, "in_off", in_off, torch.int64, dev, n_docs), rows, pool_off.data_ptr(), n_docs, max_q, total_q,
          n_q, n_kv, head_dim, head_dim ** -0.5 if scale is None else float(scale), 1 if last_tile_only else 0,
          None if order is None else order.data_ptr(), ws, ws_rows, out.data_ptr(), ldo,
-         None if lse is None else lse.data_ptr(), _stream(stream))
+         None if lse is None else lse.data_ptr(), _stream(stream, dev))
 
 
 def kalm_merged_attention_cache_rows(total_pool: int, n_docs: int) -> int:
@@ -453,7 +459,7 @@ def kalm_rms_norm(x: torch.Tensor, w: torch.Tensor, h: torch.Tensor, eps: float 
     rows, width = x.shape
     call(where, x.data_ptr(), ldx, _vec(where, "w", w, torch.bfloat16, dev, width), h.data_ptr(),
          _mat(where, "h", h, torch.bfloat16, dev, rows, width), rows, width, float(eps), float(weight_offset),
-         _stream(stream))
+         _stream(stream, dev))
 
 
 def kalm_norm_residual(y: torch.Tensor, x: torch.Tensor, x_out: torch.Tensor, h: Optional[torch.Tensor] = None,
@@ -486,7 +492,7 @@ def kalm_norm_residual(y: torch.Tensor, x: torch.Tensor, x_out: torch.Tensor, h:
          _vec(where, "q_off", q_off, torch.int64, dev, n_docs + 1), n_docs, float(residual_scale), x_out.data_ptr(),
          _mat(where, "x_out", x_out, bf16, dev, rows, width), _vec(where, "w_pre", w_pre, bf16, dev, width),
          None if h is None else h.data_ptr(), 0 if h is None else _mat(where, "h", h, bf16, dev, rows, width), rows,
-         width, float(eps), float(weight_offset), _stream(stream))
+         width, float(eps), float(weight_offset), _stream(stream, dev))
 
 
 def kalm_selftest_wait_timeout(wait_ns: int, stream=None) -> None:

@@ -107,7 +107,7 @@ def load() -> ctypes.CDLL:
 
 def call(name: str, *args) -> None:
     """Call an entry point and raise KalmError on a non-zero status."""
-    lib = load()
+    lib = _lib or load()
     st = getattr(lib, name)(*args)
     if st != 0:
         raise KalmError(st, name, lib.kalm_last_error().decode(errors="replace"))
