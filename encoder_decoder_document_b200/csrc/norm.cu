@@ -13,8 +13,9 @@
 // per sum in the block form).  Pairs of values share an instruction (f32x2), which halved the issue slots
 // (121 -> 108 us at 26,077 x 2,560); a document's gate is asked for before the first sum, not after it (108 -> 90
 // us: it comes from L2, and its latency stood behind the sum's).
-// Measured (CUDA graph of calls over three sets of inputs): 12,800 x 640 15 us = 4.4 TB/s; 25,600 x 1,152 45 us =
-// 5.2 TB/s; 26,077 x 2,560 90 us = 5.9 TB/s (0.91 of the copy bandwidth).
+// Measured (CUDA graph of calls over three sets of inputs; one gate for all / a gate per document): 12,800 x 640
+// 14.0 / 14.7 us = 4.5 TB/s; 25,600 x 1,152 40.3 / 44.2 us = 5.3 TB/s; 26,077 x 2,560 83.7 / 90.4 us = 5.9 TB/s (0.90 of
+// the copy bandwidth); kalm_rms_norm of the last 44.8 us = 6.0 TB/s.
 #include <cmath>
 
 #include "kalm.h"
@@ -25,7 +26,7 @@
 namespace kalm {
 namespace {
 
-constexpr int kWarpRowThreads = 256;  // block of the warp-per-row form
+constexpr int kWarpRowThreads = 128;  // block of the warp-per-row form (256: 12,800 x 640 in 14.9 us instead of 14.0)
 constexpr int kMaxWidth = KALM_NORM_MAX_WIDTH;
 constexpr int kMaxSpan = (kMaxWidth / 8 + 159) / 160 * 32;  // threads of the widest row: five 8-column units each
 
