@@ -5,9 +5,9 @@
 //
 // Against the tensor-core path (us; one position per document, documents of 16 to 256 cached rows, one KV head):
 //   documents      1 row          2 rows         4 rows         8 rows
-//   1              5.1 / 13.3     5.8 / 13.3     8.0 / 13.3     11.8 / 13.3
-//   100            8.2 / 19.6     9.6 / 19.6     13.1 / 19.6    19.3 / 19.7
-//   1,000          44 / 112       52 / 112       76 / 112       115 / 112
+//   1              5.1 / 12.0     6.2 / 12.0     8.2 / 12.0     11.8 / 12.0
+//   100            8.5 / 17.4     9.6 / 17.4     13.1 / 17.4    19.3 / 17.5
+//   1,000          45 / 112       53 / 112       76 / 112       115 / 112
 // so four rows are the border.  Bound by the latency of the dependent loads (offsets, pages, codes) for few
 // documents and by the fp32 pipe's instructions for many (100 documents: 6.9 MB in 13.1 us).
 //

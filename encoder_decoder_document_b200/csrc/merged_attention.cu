@@ -1297,23 +1297,26 @@ extern "C" kalm_status kalm_merged_attention(const kalm_bf16* q, int64_t ldq, co
 //
 // Widening inside the attention kernel was built and measured: eight more warps wrote each tile from its codes to
 // shared memory, no workspace.  A layer of 100 documents x 128 positions (4 query tiles a document, so every
-// cached tile is widened 4 times) took 55 us against 41.5 us for the two launches (31.6 us of them the attention),
+// cached tile is widened 4 times) took 55 us against 38.5 us for the two launches (31.6 us of them the attention),
 // 100 documents x 256 positions of 8 heads 157 us against 120 us (105 us), one position per document 19 us against
-// 20 us: a tile's widening takes about 3,500 cycles of a warp pair on the schedulers that the softmax also
+// 17 us: a tile's widening takes about 3,500 cycles of a warp pair on the schedulers that the softmax also
 // needs, more than the 1,700 cycles in which the bf16 kernel consumes a tile.
 //
 // Widening kernel: a block takes some rows of a document, all heads of K and V: a warp a row at a time, sixteen
 // lanes a head vector (16 codes each), so that its loads are whole lines of the cached row and its stores 1 KB
 // runs.  Rows up to the next multiple of 64 become zeros, so that the attention's last tile of a document multiplies
 // its masked probabilities with finite values.  Bound by latency at these sizes (two dependent loads: the
-// document's offsets and pages, then the codes; 20 MB at the Nano shape in about 6 us beside the attention);
+// document's offsets and pages, then the codes; 20 MB at the Nano shape in 5.5 us alone);
 // 3 + 1/32 bytes a value.
 namespace kalm {
 namespace {
 
 constexpr int kWidenThreads = 256;
 constexpr int kWidenWarps = kWidenThreads / 32;
-constexpr int kWidenAhead = 8;  // head-vector pairs a warp loads before it widens the first
+// Head-vector pairs a warp loads before it widens the first.  Many short warps hide the latencies best: with 8 the Nano
+// layer took 41.8 us, with 4 39.0, with 2 38.5.
+constexpr int kWidenAhead = 2;
+constexpr int64_t kWidenBlocks = 8192;  // blocks of a call, about: many documents' blocks take several turns
 constexpr int kCrossPad = 64;  // between two documents' rows: room for the last tile's zeros
 
 struct WidenParams {
@@ -1384,7 +1387,7 @@ __global__ void __launch_bounds__(kWidenThreads) cache_widen_kernel(const WidenP
         if (q0 + i < steps)
           stg_words8(dst + static_cast<int64_t>(q0 + i) * (2 * kD), e4m3x16_scaled(x[i], scale_bf16x2(s[i])));
     }
-    // the grid covers what the table has places for; a document that claims more gets zeros there, flagged
+    // (a document that claims more rows than its table has places for gets zeros there, flagged)
     r0 += stride;
     if (r0 >= end) return;
     page = lane < p.warp_rows ? cache_page(p.pages, d, r0 + lane) : -1;
@@ -1473,7 +1476,9 @@ extern "C" kalm_status kalm_merged_attention_cache(
     const int warp_rows = n_kv >= kWidenAhead ? 1 : kWidenAhead / n_kv;
     const int64_t rows_max = (ld_table * page_rows + kBKV - 1) / kBKV * kBKV;  // of a document, with its zeros
     const int64_t block_rows = kWidenWarps * warp_rows;
-    const int64_t blocks = rows_max > block_rows ? (rows_max + block_rows - 1) / block_rows : 1;
+    int64_t blocks = (rows_max + block_rows - 1) / block_rows;  // a document's
+    if (blocks > kWidenBlocks / n_docs) blocks = kWidenBlocks / n_docs;
+    if (blocks < 1) blocks = 1;
     const WidenParams wp{{k_codes, v_codes}, {k_scales, v_scales}, ld_codes, ld_scales,
                          CachePages{page_table, ld_table, n_pages, __builtin_ctz(static_cast<unsigned>(page_rows))},
                          pool_off, reinterpret_cast<__nv_bfloat16*>(workspace), rows, n_kv,

@@ -441,6 +441,29 @@ def test_attention_equals_the_uncached_kernel_over_read_rows(kalm):
     np.testing.assert_array_equal(ref_lse.cpu().numpy().astype(np.float64), lse)
 
 
+@pytest.mark.parametrize("n,top", [(3000, 100), (9000, 40)])
+def test_attention_over_many_documents(kalm, n, top):
+    """More documents than the widening has blocks for each part of: bit for bit the uncached kernel over the read rows."""
+    rng = np.random.default_rng(n)
+    nc, lq, page_rows = rng.integers(0, top, n), [5] * n, 8
+    table, n_pages = make_pages(rng, nc, page_rows)
+    codes = torch.from_numpy(rng.integers(0, 0x50, (n_pages * page_rows, 512), dtype=np.uint8)).cuda()
+    scales = torch.from_numpy(rng.integers(115, 122, (n_pages * page_rows, 16), dtype=np.uint8)).cuda()
+    q_off, p_off = i64(offsets(lq)), i64(offsets(nc))
+    qkv = torch.randn(5 * n, 1536, device="cuda").bfloat16()
+    q, k, v = qkv[:, :1024], qkv[:, 1024:1280], qkv[:, 1280:]
+    kv = torch.zeros(int(nc.sum()) + 64, 512, dtype=torch.bfloat16, device="cuda")  # (rows past the last: zeros)
+    kalm.kalm_cache_read(codes, scales, p_off, i32(table), page_rows, kv)
+    out, ref = (torch.empty(5 * n, 1024, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ws = torch.full((kalm.kalm_merged_attention_cache_rows(int(nc.sum()), n), 512), float("nan"), dtype=torch.bfloat16,
+                    device="cuda")
+    kalm.kalm_merged_attention_cache(q, k, v, codes[:, :256], scales[:, :8], codes[:, 256:], scales[:, 8:], i32(table), page_rows,
+                                     q_off, p_off, 5, 4, 1, out, workspace=ws)
+    kalm.kalm_merged_attention(q, k, v, kv[:, :256], kv[:, 256:], q_off, p_off, 5, 4, 1, ref)
+    assert torch.equal(out, ref) and bool(torch.isfinite(out).all())
+    assert kalm.kalm_check_device_errors() == 0
+
+
 def test_attention_bad_pages_and_short_workspace(kalm):
     """Rows without a page count as zeros and are flagged, in both forms; a workspace that is too short is flagged."""
     for lq in ([40, 3], [1, 1]):
