@@ -358,6 +358,7 @@ def kalm_cache_write(src: torch.Tensor, row_off: torch.Tensor, page_table: torch
     [n_docs][pages]; codes uint8 [n_pages * page_rows][width]; scales uint8 [same rows][width / 32].
     No two rows may have the same place."""
     where = "kalm_cache_write"
+    page_rows = int(page_rows)
     dev = _device(where, src)
     ld_src = _mat(where, "src", src, torch.bfloat16, dev)
     rows, width = src.shape
@@ -373,6 +374,7 @@ def kalm_cache_read(codes: torch.Tensor, scales: torch.Tensor, row_off: torch.Te
     """Read cached rows back into packed bf16 rows: dst[row_off[d] + i] = row first_row[d] + i of
     document d (the stored values exactly).  Arguments as kalm_cache_write."""
     where = "kalm_cache_read"
+    page_rows = int(page_rows)
     dev = _device(where, dst)
     ld_dst = _mat(where, "dst", dst, torch.bfloat16, dev)
     rows, width = dst.shape

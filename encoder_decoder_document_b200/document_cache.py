@@ -34,14 +34,16 @@ class CacheView:
 
 
 class DocumentCache:
-    """``n_pages`` pages of ``page_rows`` rows of ``width`` values (a multiple of 32)."""
+    """``n_pages`` pages of ``page_rows`` rows of ``width`` values (a multiple of 32).  ``layout`` says what a row's
+    columns are, for callers to compare (the cache itself does not read it)."""
 
-    def __init__(self, n_pages: int, width: int, page_rows: int = 64, device="cuda"):
+    def __init__(self, n_pages: int, width: int, page_rows: int = 64, device="cuda", layout: Hashable = None):
         if n_pages < 0 or width <= 0 or width % CACHE_GROUP:
             raise ValueError(f"DocumentCache: n_pages={n_pages}, width={width} (a positive multiple of {CACHE_GROUP})")
         if page_rows not in (8, 16, 32, 64, 128, 256, 512, 1024):
             raise ValueError(f"DocumentCache: page_rows={page_rows} is not a power of two in [8, 1024]")
         self.n_pages, self.width, self.page_rows, self.device = n_pages, width, page_rows, torch.device(device)
+        self.layout = layout
         self.codes = torch.zeros(n_pages * page_rows, width, dtype=torch.uint8, device=device)
         self.scales = torch.zeros(n_pages * page_rows, width // CACHE_GROUP, dtype=torch.uint8, device=device)
         self._free = list(range(n_pages - 1, -1, -1))  # taken from the end: page 0 first

@@ -618,7 +618,10 @@ class FBNLScorer:
     def new_cache(self, n_pages: int, page_rows: int = 64, device="cuda") -> DocumentCache:
         """A cache for this stack: a row holds the cross K/V of every layer of one pooled vector
         (kalm_cross_kv_proj's layout) in 8 bits, n_layers * 2 * n_kv * head_dim * 33 / 32 bytes."""
-        return DocumentCache(n_pages, self.L * 2 * self.n_kv * self.D, page_rows, device)
+        return DocumentCache(n_pages, self.L * 2 * self.n_kv * self.D, page_rows, device, self._cache_layout())
+
+    def _cache_layout(self) -> tuple:
+        return ("cross K/V", self.L, self.n_kv, self.D)
 
     def cache_put(self, cache: DocumentCache, keys, enc: np.ndarray, doc_len: np.ndarray) -> None:
         """Pool documents, project their cross K/V and store them under ``keys``; arguments as for
@@ -680,9 +683,8 @@ class FBNLScorer:
         return rank(res[:, 2], res[:, 3], top_n)
 
     def _check_cache(self, cache: DocumentCache) -> None:
-        width = self.L * 2 * self.n_kv * self.D
-        if cache.width != width:
-            raise ValueError(f"the cache's rows have {cache.width} values, this stack's cross K/V {width}")
+        if cache.layout != self._cache_layout():
+            raise ValueError(f"the cache's rows are {cache.layout}, this stack's {self._cache_layout()}: use new_cache()")
 
     def check_errors(self) -> None:
         """Wait for this scorer's streams and raise ``KalmError`` if a kernel recorded a
