@@ -298,7 +298,7 @@ def run_attention(kalm, a, scale=1 / 16, order=None, in_off=None, last=False, po
     rows = a["q"].shape[0]
     q_off, p_off = i64(a["q_off"]), i64(a["p_off"])
     r = int(a["q_off"][-1])
-    qkv = torch.cat([f64_to_dev(a[k].reshape(rows, -1)) for k in ("q", "ks", "vs")], 1)
+    qkv = torch.cat([f64_to_dev(a[k].reshape(rows, a[k].shape[1] * d)) for k in ("q", "ks", "vs")], 1)
     w, win = n_kv * d, a["window"]
     n = a["codes"].shape[0]
     codes = torch.full((n, win + 2 * w), 0x7F, dtype=torch.uint8, device="cuda")
@@ -735,3 +735,69 @@ def test_numpy_numbers_as_sizes(kalm):
     got, _ = run_attention(kalm, a, scale=np.float32(1 / 16), max_q=np.int64(20))
     want, _ = run_attention(kalm, a)
     np.testing.assert_array_equal(got, want)
+
+
+@pytest.mark.parametrize("lq,nc,n_q,n_kv,page_rows", [
+    ([3, 40], [5000, 1], 4, 1, 256),       # a document far longer than the passages' limit
+    ([1, 1], [5000, 4097], 4, 1, 8),
+    ([0, 0], [10, 20], 4, 1, 16),          # no decoder rows at all
+    ([], [], 4, 1, 16),                    # no documents
+    ([20, 0, 7], [30, 40, 0], 16, 1, 16),  # 16 query heads per KV head
+])
+def test_attention_outer_sizes(kalm, lq, nc, n_q, n_kv, page_rows):
+    a = attention(np.random.default_rng(sum(nc)), lq, nc, n_q, n_kv, page_rows)
+    got, lse = run_attention(kalm, a, poison=True, max_q=max(lq, default=0) or 1)
+    want, want_lse, vmax = plain_attention(a)
+    if got.size:
+        check(got, lse, want, want_lse, vmax)
+    assert got.shape == want.shape and kalm.kalm_check_device_errors() == 0
+
+
+def test_few_rows_shared_inputs_and_last_tile(kalm):
+    """The few-row form with shared decoder rows; its last-tile mode computes every row (they fit one tile)."""
+    a = attention(np.random.default_rng(35), [2] * 5, [5, 130, 0, 64, 9], 2, 1, 16)
+    for k in ("q", "ks", "vs"):
+        a[k] = a[k][:2]
+    want, want_lse, vmax = plain_attention(a, in_off=[0] * 5)
+    got, lse = run_attention(kalm, a, in_off=[0] * 5)
+    check(got, lse, want, want_lse, vmax)
+    last, _ = run_attention(kalm, a, in_off=[0] * 5, last=True)
+    np.testing.assert_array_equal(last, got)
+    assert kalm.kalm_check_device_errors() == 0
+
+
+def test_few_rows_flag_more_rows_than_sized_for(kalm):
+    """A document with more decoder rows than max_q, or rows past the inputs: flagged, its output left alone."""
+    a = attention(np.random.default_rng(36), [1, 3, 1], [9, 9, 9], 1, 1, 16)
+    got, _ = run_attention(kalm, a, max_q=2)
+    with pytest.raises(kalm.KalmError):
+        kalm.kalm_check_device_errors()
+    assert np.isnan(got[1:4]).all() and np.isfinite(got[[0, 4]]).all()
+
+
+def test_twenty_thousand_documents(kalm):
+    """Offsets of more documents than two rounds of the search: single rows written, read, and normed with a gate each."""
+    n, width = 20000, 32
+    rng = np.random.default_rng(37)
+    rows = rng.integers(0, 3, n)
+    off = offsets(rows)
+    total = int(off[-1])
+    v = rand_bf16(rng, (total, width))
+    table = rng.permutation(n).astype(np.int32)[:, None]
+    codes = torch.zeros(n * 8, width, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(n * 8, 1, dtype=torch.uint8, device="cuda")
+    first = rng.integers(0, 6, n)
+    kalm.kalm_cache_write(f64_to_dev(v), i64(off), i32(table), 8, codes, scales, first_row=i32(first))
+    c, s = quantise(v)
+    at = np.concatenate([table[d, 0] * 8 + first[d] + np.arange(rows[d]) for d in range(n)])
+    np.testing.assert_array_equal(codes.cpu().numpy()[at], c)
+    np.testing.assert_array_equal(scales.cpu().numpy()[at], s)
+    back = torch.empty(total, width, dtype=torch.bfloat16, device="cuda")
+    kalm.kalm_cache_read(codes, scales, i64(off), i32(table), 8, back, first_row=i32(first))
+    np.testing.assert_array_equal(from_dev(back), dequantise(c, s))
+    gate = rand_bf16(rng, (n, width))
+    out = torch.empty(total, width, dtype=torch.bfloat16, device="cuda")
+    kalm.kalm_norm_residual(f64_to_dev(v), torch.zeros_like(out), out, gate=f64_to_dev(gate), q_off=i64(off))
+    want = oracle.bf16_round(v * np.repeat(gate, rows, 0))  # exact products of bf16 numbers, one rounding
+    np.testing.assert_array_equal(from_dev(out), want)
+    assert kalm.kalm_check_device_errors() == 0

@@ -246,3 +246,28 @@ def test_norm_options_that_do_not_go_together(kalm):
 def kalm_cache_of(width):
     from encoder_decoder_document_b200.document_cache import DocumentCache
     return DocumentCache(1, width)
+
+
+def test_pooled_vectors_in_a_cache(kalm):
+    """The other use of a cache: pooled vectors kept in 8 bits, read back and projected for a query."""
+    from encoder_decoder_document_b200.document_cache import DocumentCache
+    q = synthetic.make_query("tiny", layers=2)
+    pooled, off = oracle.chunk_pool(bf(q.enc), q.tok_off, q.doc_len)
+    counts = np.diff(off)
+    cache = DocumentCache(12, q.hidden, page_rows=8)
+    dev = to_dev(oracle.f64_to_bf16_bits(pooled))
+    cache.put(range(4), counts, dev)
+    cache.append([2], [3], dev[:3])
+    cache.drop([1])
+    codes, scales = quantise(pooled)
+    from tests.test_gpu_cache import dequantise
+    val = dequantise(codes, scales)
+    rows, row_off = cache.get([2, 0])
+    want = np.concatenate([val[off[2]:off[3]], val[:3], val[off[0]:off[1]]])
+    np.testing.assert_array_equal(from_dev(rows), want)
+    assert row_off.tolist() == [0, counts[2] + 3, counts[2] + 3 + counts[0]]
+    kv = torch.empty(rows.shape[0], q.layers * 2 * q.n_kv * q.head_dim, dtype=torch.bfloat16, device="cuda")
+    kalm.kalm_cross_kv_proj(rows, to_dev(q.weights.w_kv_cross), kv, q.n_kv)
+    ref = oracle.linear(want, bf(q.weights.w_kv_cross).reshape(-1, q.hidden))
+    assert (np.abs(from_dev(kv) - ref) <= 2.0 ** -7 * np.abs(ref) + 1e-4).all()  # one bf16 step of the projection
+    kalm.kalm_check_device_errors()
