@@ -94,7 +94,7 @@ def _mat(where: str, name: str, t: torch.Tensor, dtype: torch.dtype, dev: int, r
 
 def _pair(where: str, name: str, k: torch.Tensor, v: torch.Tensor) -> None:
     """The V tensor of a K / V pair is laid out as its (checked) K."""
-    if v.dtype is not k.dtype or v.device != k.device or v.shape != k.shape or v.stride() != k.stride():
+    if v.shape != k.shape or v.stride() != k.stride() or v.dtype is not k.dtype or v.get_device() != k.get_device():
         raise KalmError(1, where, f"{name}: K is {k.dtype} {tuple(k.shape)} with strides {k.stride()} on {k.device}, V "
                                   f"{v.dtype} {tuple(v.shape)} with strides {v.stride()} on {v.device}")
 
@@ -333,19 +333,22 @@ def kalm_linear_rope(x: torch.Tensor, w: torch.Tensor, y: torch.Tensor, q_off: t
 def _cache_args(where: str, dev: int, row_off: torch.Tensor, page_table: torch.Tensor, page_rows: int,
                 codes: torch.Tensor, scales: torch.Tensor, width: int):
     """Checks what the calls on a document cache share; (n_docs, ld_table, n_pages, ld_codes, ld_scales)."""
-    n_docs = row_off.numel() - 1
+    if row_off.dtype is not torch.int64 or row_off.get_device() != dev or row_off.dim() != 1 or \
+            not row_off.is_contiguous():
+        _refuse(where, "offsets", row_off, torch.int64, dev, "expected a contiguous vector")
+    n_docs = len(row_off) - 1
     if n_docs < 0:
         raise KalmError(1, where, "the offsets are empty")
-    _vec(where, "offsets", row_off, torch.int64, dev, n_docs + 1)
-    if page_table.dtype is not torch.int32 or page_table.get_device() != dev or page_table.dim() != 2 or \
-            page_table.shape[0] != n_docs or not page_table.is_contiguous():
+    shape = page_table.shape
+    if page_table.dtype is not torch.int32 or page_table.get_device() != dev or len(shape) != 2 or \
+            shape[0] != n_docs or not page_table.is_contiguous():
         _refuse(where, "page_table", page_table, torch.int32, dev, f"expected a contiguous [{n_docs}][pages] tensor")
     ld_codes = _mat(where, "codes", codes, torch.uint8, dev, -1, width)
-    cached = codes.shape[0]
+    cached = len(codes)
     if page_rows <= 0 or cached % page_rows:
         raise KalmError(1, where, f"{cached} cache rows are not whole pages of {page_rows}")
     ld_scales = _mat(where, "scales", scales, torch.uint8, dev, cached, width // CACHE_GROUP)
-    return n_docs, page_table.shape[1], cached // page_rows, ld_codes, ld_scales
+    return n_docs, shape[1], cached // page_rows, ld_codes, ld_scales
 
 
 def kalm_cache_write(src: torch.Tensor, row_off: torch.Tensor, page_table: torch.Tensor, page_rows: int,
@@ -405,7 +408,7 @@ def kalm_merged_attention_cache(q: torch.Tensor, k_self: torch.Tensor, v_self: t
     bf16 = torch.bfloat16
     max_q, page_rows = int(max_q), int(page_rows)
     dev = _device(where, q)
-    width, rows = n_kv * head_dim, q.shape[0]
+    width, rows = n_kv * head_dim, len(q)
     n_docs, ld_table, n_pages, ld_codes, ld_scales = _cache_args(where, dev, pool_off, page_table, page_rows, k_codes,
                                                                  k_scales, width)
     ld_self = _mat(where, "k_self", k_self, bf16, dev, rows, width)
@@ -414,9 +417,9 @@ def kalm_merged_attention_cache(q: torch.Tensor, k_self: torch.Tensor, v_self: t
     _pair(where, "scales", k_scales, v_scales)
     ldq = _mat(where, "q", q, bf16, dev, rows, n_q * head_dim)
     ldo = _mat(where, "out", out, bf16, dev, -1, n_q * head_dim)
-    total_q = out.shape[0] if total_q is None else int(total_q)
-    if total_q > out.shape[0] or (in_off is None and total_q > rows):
-        raise KalmError(1, where, f"total_q={total_q} exceeds the rows of out ({out.shape[0]}) or q ({rows})")
+    total_q = len(out) if total_q is None else int(total_q)
+    if total_q > len(out) or (in_off is None and total_q > rows):
+        raise KalmError(1, where, f"total_q={total_q} exceeds the rows of out ({len(out)}) or q ({rows})")
     if lse is not None and (lse.dtype is not torch.float32 or lse.get_device() != dev or lse.dim() != 2 or
                             lse.shape[0] < total_q or lse.shape[1] != n_q or not lse.is_contiguous()):
         _refuse(where, "lse", lse, torch.float32, dev, f"expected a contiguous [{total_q}][{n_q}] tensor")
@@ -430,14 +433,14 @@ def kalm_merged_attention_cache(q: torch.Tensor, k_self: torch.Tensor, v_self: t
     if workspace is None and max_q * n_q > CACHE_FEW_ROWS * n_kv:
         shape = (n_docs * (ld_table * page_rows + 64), 2 * width)  # every place of the table, see the rows helper below
         if stream is None:
-            workspace = torch.empty(shape, dtype=bf16, device=q.device)
+            workspace = q.new_empty(shape)
         else:
             with torch.cuda.stream(stream):  # the allocator hands memory out per stream
-                workspace = torch.empty(shape, dtype=bf16, device=q.device)
+                workspace = q.new_empty(shape)
     elif workspace is not None and _mat(where, "workspace", workspace, bf16, dev, -1, 2 * width) != 2 * width:
         raise KalmError(1, where, "the workspace must be contiguous")
     if workspace is not None:
-        ws, ws_rows = workspace.data_ptr(), workspace.shape[0]
+        ws, ws_rows = workspace.data_ptr(), len(workspace)
     call(where, q.data_ptr(), ldq, k_self.data_ptr(), v_self.data_ptr(), ld_self, k_codes.data_ptr(),
          v_codes.data_ptr(), ld_codes, k_scales.data_ptr(), v_scales.data_ptr(), ld_scales, page_table.data_ptr(),
          ld_table, page_rows, n_pages, _vec(where, "q_off", q_off, torch.int64, dev, n_docs + 1),
