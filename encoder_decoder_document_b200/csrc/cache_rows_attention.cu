@@ -6,10 +6,10 @@
 // Against the tensor-core path (us; one position per document, documents of 16 to 256 cached rows, one KV head):
 //   documents      1 row          2 rows         4 rows         8 rows
 //   1              5.1 / 12.0     6.2 / 12.0     8.2 / 12.0     11.8 / 12.0
-//   100            8.5 / 17.4     9.6 / 17.4     13.1 / 17.4    19.3 / 17.5
-//   1,000          45 / 112       53 / 112       76 / 112       115 / 112
+//   100            8.5 / 17.4     9.6 / 17.4     13.3 / 17.4    19.3 / 17.5
+//   1,000          45 / 112       52 / 112       77 / 112       115 / 112
 // so four rows are the border.  Bound by the latency of the dependent loads (offsets, pages, codes) for few
-// documents and by the fp32 pipe's instructions for many (100 documents: 6.9 MB in 13.1 us).
+// documents and by the fp32 pipe's instructions for many (100 documents: 6.9 MB in 13.3 us).
 //
 // One block per (document, KV head), eight warps.  For each packed row r and visible key j
 //   s = scale * q_r . k_j;   out_r = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m)
@@ -54,7 +54,7 @@ __device__ __forceinline__ void unpack_e4m3x8(const uint2& v, F2 (&f)[4]) {
 constexpr int log2_of(int n) { return n <= 1 ? 0 : 1 + log2_of(n / 2); }
 
 // R packed rows (1, 2 or 4), KEYS keys at a time; R * KEYS <= 32.  (4 keys at a time: 9.2, 10.6, 13.3 us for 1, 2, 4 rows of 100
-// documents against 8.2, 9.6, 13.1.)
+// documents against 8.4, 9.6, 13.1 then.)
 template <int R>
 struct Few {
   static constexpr int KEYS = 8;
@@ -70,11 +70,12 @@ struct State {
 };
 
 // One group of keys: their 8 columns in this lane (k, v as fp32 numbers, times ks, vs), `seen`: whether this
-// lane's (key, row) counts.
+// lane's (key, row) counts.  G > 0: self keys from position 0 on, row r (position r / G) sees key j if j * G <= r, and what it
+// does not see is left out of its output altogether (0 * NaN would be NaN).
 template <int R>
 __device__ __forceinline__ void attend(State<R>& st, const F2 (&k)[Few<R>::KEYS][4], const float (&ks)[Few<R>::KEYS],
                                        const F2 (&v)[Few<R>::KEYS][4], const float (&vs)[Few<R>::KEYS], bool seen,
-                                       int lane) {
+                                       int lane, int G = 0) {
   constexpr int KEYS = Few<R>::KEYS, N = Few<R>::N, DUP = Few<R>::DUP;
   float part[N];
 #pragma unroll
@@ -129,6 +130,7 @@ __device__ __forceinline__ void attend(State<R>& st, const F2 (&k)[Few<R>::KEYS]
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const float pj = __shfl_sync(0xffffffffu, p, (j * R + r) << DUP) * vs[j];
+      if (j * G > r) continue;
 #pragma unroll
       for (int e = 0; e < 4; ++e) st.acc[r][e] = fma2(pair2(pj, pj), v[j][e], st.acc[r][e]);
     }
@@ -190,7 +192,8 @@ __global__ void __launch_bounds__(kWarps * 32) cache_rows_attention_kernel(const
   const int64_t nc = __ldg(p.pool_off + d + 1) - c0;
   const int64_t in0 = p.in_off ? __ldg(p.in_off + d) : q0;
   if (lq <= 0) return;
-  if (lq > p.max_q || in0 < 0 || in0 + lq > p.total_in) {  // more rows than the call was sized for, or rows that do not exist
+  // more rows than the call was sized for, or rows (of q and self K / V, or of the output) that do not exist
+  if (lq > p.max_q || in0 < 0 || in0 + lq > p.total_in || q0 < 0 || q0 + lq > p.total_q) {
     if (threadIdx.x == 0) record_error(p.err, kErrDeviceArg | kSiteAttention);
     return;
   }
@@ -224,23 +227,22 @@ __global__ void __launch_bounds__(kWarps * 32) cache_rows_attention_kernel(const
 
   // the last warp takes the self keys (at most R), the row's position and those before it
   if (warp == kWarps - 1) {
-    for (int j0 = 0; j0 < static_cast<int>(lq); j0 += KEYS) {
-      F2 k[KEYS][4], v[KEYS][4];
-      float one[KEYS];
+    static_assert(KEYS >= KALM_CACHE_FEW_ROWS, "one group holds the self keys");
+    F2 k[KEYS][4], v[KEYS][4];
+    float one[KEYS];
 #pragma unroll
-      for (int j = 0; j < KEYS; ++j) {
-        uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-        if (j0 + j < static_cast<int>(lq)) {
-          const int64_t at = (in0 + j0 + j) * p.ld_self + static_cast<int64_t>(head) * kHeadDim + lane * 8;
-          a = *reinterpret_cast<const uint4*>(p.k_self + at);
-          b = *reinterpret_cast<const uint4*>(p.v_self + at);
-        }
-        unpack_bf16x8(a, k[j]);
-        unpack_bf16x8(b, v[j]);
-        one[j] = 1.f;
+    for (int j = 0; j < KEYS; ++j) {
+      uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+      if (j < static_cast<int>(lq)) {
+        const int64_t at = (in0 + j) * p.ld_self + static_cast<int64_t>(head) * kHeadDim + lane * 8;
+        a = *reinterpret_cast<const uint4*>(p.k_self + at);
+        b = *reinterpret_cast<const uint4*>(p.v_self + at);
       }
-      attend<R>(st, k, one, v, one, my_row < rows && j0 + my_key <= my_row / p.G, lane);
+      unpack_bf16x8(a, k[j]);
+      unpack_bf16x8(b, v[j]);
+      one[j] = 1.f;
     }
+    attend<R>(st, k, one, v, one, my_row < rows && my_key * p.G <= my_row, lane, p.G);
   }
   while (next.n > 0) {
     const Group<R> cur = next;

@@ -14,7 +14,7 @@ struct CacheRowsParams {
   int64_t ldq, ld_self, ld_codes, ld_scales, ldo;
   CachePages pages;
   const int64_t *q_off, *in_off, *pool_off;
-  int64_t total_in;
+  int64_t total_in, total_q;  // rows of q and self K / V, of the output
   int32_t n_q, n_kv, G, max_q;
   float scale_log2;  // scale * log2(e)
   __nv_bfloat16* out;

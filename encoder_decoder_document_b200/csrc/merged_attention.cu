@@ -1462,6 +1462,7 @@ extern "C" kalm_status kalm_merged_attention_cache(
     p.in_off = in_off;
     p.pool_off = pool_off;
     p.total_in = in_off ? total_in : total_q;
+    p.total_q = total_q;
     p.n_q = n_q;
     p.n_kv = n_kv;
     p.G = n_q / n_kv;

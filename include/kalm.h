@@ -541,8 +541,9 @@ kalm_status kalm_cache_read(const uint8_t* codes, int64_t ld_codes, const uint8_
  *          NULL with 0 rows where ld_table is 0 (nothing cached) or the rows are few.
  * Other documents' rows, self or cached, and what lies behind a document's last
  * row have no influence, NaN and infinities included.  Within a document, a NaN or
- * infinity in a self V row can also reach the decoder rows before it (the mask
- * makes its probability zero, and 0 * NaN is NaN).
+ * infinity in a self V row has none on the decoder rows before it in a call of few
+ * rows; in other calls it can reach them (the mask makes its probability zero, and
+ * 0 * NaN is NaN).
  * At most 65,535 documents a call of more than few rows. */
 kalm_status kalm_merged_attention_cache(const kalm_bf16* q, int64_t ldq, const kalm_bf16* k_self,
                                         const kalm_bf16* v_self, int64_t ld_self, const uint8_t* k_codes,

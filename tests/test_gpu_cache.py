@@ -801,3 +801,34 @@ def test_twenty_thousand_documents(kalm):
     want = oracle.bf16_round(v * np.repeat(gate, rows, 0))  # exact products of bf16 numbers, one rounding
     np.testing.assert_array_equal(from_dev(out), want)
     assert kalm.kalm_check_device_errors() == 0
+
+
+@pytest.mark.parametrize("lq,n_q,n_kv", [([4, 3], 1, 1), ([2, 2], 4, 2)])
+def test_few_rows_do_not_see_later_values(kalm, lq, n_q, n_kv):
+    """A NaN in a self K / V row stays out of the decoder rows before it; those after it have it."""
+    a = attention(np.random.default_rng(40), lq, [30, 70], n_q, n_kv, 16)
+    want, want_lse, vmax = plain_attention(a)
+    last = lq[0] - 1  # of the first document
+    a["vs"][last] = np.nan
+    a["ks"][last] = np.nan
+    got, lse = run_attention(kalm, a)
+    assert np.isnan(got[last]).all() and np.isnan(lse[last]).all()
+    keep = np.arange(sum(lq)) != last
+    check(got[keep], lse[keep], want[keep], want_lse[keep], vmax[keep])
+    assert kalm.kalm_check_device_errors() == 0
+
+
+def test_few_rows_stay_inside_the_output(kalm):
+    """A document whose rows lie past total_q (its inputs do exist): flagged, the rows behind total_q left alone."""
+    a = attention(np.random.default_rng(41), [1, 1, 1], [9, 9, 9], 1, 1, 16)
+    d = 256
+    q, ks, vs = (f64_to_dev(a[k].reshape(3, d)) for k in ("q", "ks", "vs"))
+    codes, scales = torch.from_numpy(a["codes"]).cuda(), torch.from_numpy(a["scales"]).cuda()
+    out = torch.full((3, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    kalm.kalm_merged_attention_cache(q, ks, vs, codes[:, :d], scales[:, :d // 32], codes[:, d:], scales[:, d // 32:],
+                                     i32(a["table"]), 16, i64(a["q_off"]), i64(a["p_off"]), 1, 1, 1, out,
+                                     in_off=i64([0, 1, 2]), total_q=2)
+    with pytest.raises(kalm.KalmError):
+        kalm.kalm_check_device_errors()
+    got = from_dev(out)
+    assert np.isfinite(got[:2]).all() and np.isnan(got[2]).all()
