@@ -14,8 +14,8 @@
 // (121 -> 108 us at 26,077 x 2,560); a document's gate is asked for before the first sum, not after it (108 -> 90
 // us: it comes from L2, and its latency stood behind the sum's).
 // Measured (CUDA graph of calls over three sets of inputs; one gate for all / a gate per document): 12,800 x 640
-// 14.0 / 14.7 us = 4.5 TB/s; 25,600 x 1,152 40.3 / 44.2 us = 5.3 TB/s; 26,077 x 2,560 83.7 / 90.4 us = 5.9 TB/s (0.90 of
-// the copy bandwidth); kalm_rms_norm of the last 44.8 us = 6.0 TB/s.
+// 13.6 / 14.7 us = 4.5 TB/s; 25,600 x 1,152 39.8 / 42.0 us = 5.6 TB/s; 26,077 x 2,560 82.9 / 87.5 us = 6.1 TB/s (0.93 of
+// the copy bandwidth); 8,000 x 8,192 85.8 / 94.5 us = 5.5 TB/s; kalm_rms_norm of 26,077 x 2,560 40.8 us = 6.5 TB/s.
 #include <cmath>
 
 #include "kalm.h"
@@ -26,18 +26,19 @@
 namespace kalm {
 namespace {
 
-constexpr int kWarpRowThreads = 128;  // block of the warp-per-row form (256: 12,800 x 640 in 14.9 us instead of 14.0)
+constexpr int kWarpRowThreads = 128;  // block of the warp-per-row form (256: 12,800 x 640 in 14.9 us instead of 14.0 then)
 constexpr int kMaxWidth = KALM_NORM_MAX_WIDTH;
-constexpr int kMaxSpan = (kMaxWidth / 8 + 159) / 160 * 32;  // threads of the widest row: five 8-column units each
+constexpr int kBlockRow = 448;                // threads of a block-per-row block, at most
+constexpr int kWideRow = kMaxWidth / 8 / 4;   // and of the widest rows': four 8-column units each
 
 struct NormParams {
-  const uint4* y;       // block output, or NULL: a norm of x alone
+  const uint4* y;       // block output (NULL: a norm of x alone)
   const uint4* x;       // residual stream
   const uint4* w_post;  // NULL: y enters as it is
   const uint4* gate;    // NULL: 1
   const uint4* w_pre;
-  uint4* x_out;         // NULL: not written
-  uint4* h;             // NULL: not written
+  uint4* x_out;         // where y is
+  uint4* h;             // NULL: not written (where y is)
   const int64_t* q_off; // rows of each document; NULL: all rows
   int64_t ldy, ldx, ld_gate, ldxo, ldh;  // in 16-byte units
   int64_t rows;
@@ -51,15 +52,15 @@ __device__ __forceinline__ uint32_t pack2(F2 v) {
   return pack_bf16x2(f.x, f.y);
 }
 
-// A row's sum over its SPAN threads: SPAN lanes of a warp (a power of two), or the whole block where SPAN
-// is 0 (through `part`, one slot per warp).
+// A row's sum over its threads: SPAN lanes of a warp (a power of two), or the whole block where SPAN is more than a warp
+// (through `part`, one slot per warp).
 template <int SPAN>
 __device__ __forceinline__ float row_sum(F2 v2, float* part) {
   const float2 f = split2(v2);
   float v = f.x + f.y;
 #pragma unroll
-  for (int o = (SPAN ? SPAN : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (!SPAN) {
+  for (int o = (SPAN <= 32 ? SPAN : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (SPAN > 32) {
     const int warps = blockDim.x >> 5;
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
@@ -69,27 +70,37 @@ __device__ __forceinline__ float row_sum(F2 v2, float* part) {
   return v;
 }
 
-// V: 8-column units a thread holds; unit i of thread t is i * (threads of the row) + t.
-template <int V, int SPAN>
-__global__ void __launch_bounds__(SPAN ? kWarpRowThreads : kMaxSpan) norm_kernel(const NormParams p) {
+// V: 8-column units a thread holds; unit i of thread t is i * (threads of the row) + t.  SPAN: lanes of a row, or the most
+// threads of its block.  SUM: y is there (else a norm of x alone, whose fewer registers let more rows be in flight:
+// 26,077 x 2,560 in 40.9 us instead of 44.8).
+// Registers are bounded where that makes room for one more warp or block on an SM at (nearly) no spill; at a gate per
+// document, without and with: five units a lane of a warp 44.0 and 41.9 us (25,600 x 1,152), four of a block 98 and 95
+// (8,000 x 8,192), four of the widest rows' 141 and 106 (4,000 x 16,384; the next smaller form has one block an SM there).
+template <int V, int SPAN, bool SUM>
+__global__ void __launch_bounds__(SPAN <= 32 ? kWarpRowThreads : SPAN, SPAN == 32 && V == 5  ? 7
+                                                                     : SPAN > 32 && V == 4 ? 2
+                                                                                           : 0)
+    norm_kernel(const NormParams p) {
   pdl_launch_dependents();
   pdl_wait_predecessor();
-  __shared__ float part[2][kMaxSpan / 32];
+  __shared__ float part[2][SPAN <= 32 ? 1 : SPAN / 32];
   const int lane = threadIdx.x & 31;
-  const int span = SPAN ? SPAN : blockDim.x;
-  const int t = SPAN ? lane & (SPAN - 1) : threadIdx.x;
-  const int64_t row = SPAN ? (static_cast<int64_t>(blockIdx.x) * kWarpRowThreads + threadIdx.x) / (SPAN ? SPAN : 1)
-                           : static_cast<int64_t>(blockIdx.x);
+  constexpr bool kLanes = SPAN <= 32;
+  const int span = kLanes ? SPAN : blockDim.x;
+  const int t = kLanes ? lane & (SPAN - 1) : threadIdx.x;
+  const int64_t row = kLanes ? (static_cast<int64_t>(blockIdx.x) * kWarpRowThreads + threadIdx.x) / SPAN
+                             : static_cast<int64_t>(blockIdx.x);
   // rows of no document, or past the last, are computed as zeros (their threads take part in the shuffles) and not written
   bool there = row < p.rows;
   // The row's document: up to 32 threads search together, four offsets each a round.  The first round's
   // offsets are asked for before x and y: loads come back in order, so that up to 128 documents cost the
   // latency of no load but the gate's own.
-  constexpr int kWays = SPAN ? SPAN : 32;
+  constexpr int kWays = kLanes ? SPAN : 32;
   const int way = lane & (kWays - 1);
-  int lo = 0, hi = p.q_off ? p.n_docs : 0, step = max(1, (hi + 4 * kWays - 1) / (4 * kWays));
+  const bool docs = SUM && p.q_off;
+  int lo = 0, hi = docs ? p.n_docs : 0, step = max(1, (hi + 4 * kWays - 1) / (4 * kWays));
   int64_t o[4], o_first = 0, o_last = 0;
-  if (p.q_off) {
+  if (docs) {
     o_first = __ldg(p.q_off);
     o_last = __ldg(p.q_off + p.n_docs);
 #pragma unroll
@@ -98,17 +109,18 @@ __global__ void __launch_bounds__(SPAN ? kWarpRowThreads : kMaxSpan) norm_kernel
       o[j] = at < hi ? __ldg(p.q_off + at) : INT64_MAX;
     }
   }
-  uint4 xv[V], yv[V];
+  uint4 xv[V], yv[SUM ? V : 1];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = i * span + t;
-    xv[i] = yv[i] = make_uint4(0u, 0u, 0u, 0u);
+    xv[i] = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (SUM) yv[i] = xv[i];
     if (there && c < p.nv) {
       xv[i] = p.x[row * p.ldx + c];
-      if (p.y) yv[i] = p.y[row * p.ldy + c];
+      if constexpr (SUM) yv[i] = p.y[row * p.ldy + c];
     }
   }
-  if (p.q_off) {
+  if (docs) {
     there = there && row >= o_first && row < o_last;
     while (true) {
       int n = 0;
@@ -127,12 +139,12 @@ __global__ void __launch_bounds__(SPAN ? kWarpRowThreads : kMaxSpan) norm_kernel
         o[j] = at < hi ? __ldg(p.q_off + at) : INT64_MAX;
       }
     }
-    if (!SPAN && !there) return;  // the whole block's row
+    if (!kLanes && !there) return;  // the whole block's row
   }
   const int doc = lo;
   const F2 off = pair2(p.weight_offset, p.weight_offset);
   F2 r[V][4];
-  if (p.y) {
+  if constexpr (SUM) {
     uint4 gv[V];  // asked for before the first sum: a document's gate comes from L2
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -172,7 +184,7 @@ __global__ void __launch_bounds__(SPAN ? kWarpRowThreads : kMaxSpan) norm_kernel
       for (int k = 0; k < 4; ++k) r[i][k] = unpack2((&xv[i].x)[k]);
   }
   float rs = 0.f;
-  if (p.h) {
+  if (!SUM || p.h) {
     F2 ss = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -185,9 +197,9 @@ __global__ void __launch_bounds__(SPAN ? kWarpRowThreads : kMaxSpan) norm_kernel
   for (int i = 0; i < V; ++i) {
     const int c = i * span + t;
     if (!there || c >= p.nv) continue;
-    if (p.x_out)
+    if (SUM)
       p.x_out[row * p.ldxo + c] = make_uint4(pack2(r[i][0]), pack2(r[i][1]), pack2(r[i][2]), pack2(r[i][3]));
-    if (p.h) {
+    if (!SUM || p.h) {
       const uint4 wv = __ldg(p.w_pre + c);
       uint32_t o[4];
 #pragma unroll
@@ -197,29 +209,37 @@ __global__ void __launch_bounds__(SPAN ? kWarpRowThreads : kMaxSpan) norm_kernel
   }
 }
 
-template <int SPAN>
+template <int SPAN, bool SUM>
 cudaError_t launch_norm(int v, dim3 grid, dim3 block, cudaStream_t s, const NormParams& p) {
-  switch (v) {
-    case 1: return launch_pdl(norm_kernel<1, SPAN>, grid, block, 0, s, p);
-    case 2: return launch_pdl(norm_kernel<2, SPAN>, grid, block, 0, s, p);
-    case 3: return launch_pdl(norm_kernel<3, SPAN>, grid, block, 0, s, p);
-    case 4: return launch_pdl(norm_kernel<4, SPAN>, grid, block, 0, s, p);
-    default: return launch_pdl(norm_kernel<5, SPAN>, grid, block, 0, s, p);
+  if constexpr (SPAN == kWideRow) {
+    return launch_pdl(norm_kernel<4, SPAN, SUM>, grid, block, 0, s, p);
+  } else {
+    if constexpr (SPAN <= 32) {  // (a block's threads have three units at least)
+      if (v == 1) return launch_pdl(norm_kernel<1, SPAN, SUM>, grid, block, 0, s, p);
+      if (v == 2) return launch_pdl(norm_kernel<2, SPAN, SUM>, grid, block, 0, s, p);
+    }
+    return v <= 3   ? launch_pdl(norm_kernel<3, SPAN, SUM>, grid, block, 0, s, p)
+           : v == 4 ? launch_pdl(norm_kernel<4, SPAN, SUM>, grid, block, 0, s, p)
+                    : launch_pdl(norm_kernel<5, SPAN, SUM>, grid, block, 0, s, p);
   }
 }
 
-kalm_status run_norm(const char* what, const NormParams& p, cudaStream_t s) {
+template <bool SUM>
+cudaError_t launch(const NormParams& p, cudaStream_t s) {
   // The fewest threads a row with at most five units each: 8 lanes, a warp, or whole warps (a block per row).  At
-  // 26,077 x 2,560 (a gate per document) 64 threads x 5 units took 90 us, 96 x 4 100, 128 x 3 98, 160 x 2 100; at
-  // 25,600 x 1,152 32 x 5 took 45 us, 64 x 3 47, 96 x 2 52; at 12,800 x 640 32 x 3 took 14 us, 16 x 5 16.
-  const int span = p.nv <= 8 ? 8 : 32 * ((p.nv + 159) / 160);
+  // 26,077 x 2,560 (a gate per document) 64 threads x 5 units took 90 us, 96 x 4 100, 128 x 3 92, 160 x 2 94; at
+  // 25,600 x 1,152 32 x 5 took 44 us, 64 x 3 47, 96 x 2 52; at 12,800 x 640 32 x 3 took 14 us, 16 x 5 16.  Wide rows have
+  // four: their blocks are large, and with five fewer of them fit an SM (9,000 x 7,168: 224 x 4 89 us, 192 x 5 95;
+  // 8,000 x 8,192: 256 x 4 96 us, 224 x 5 103, 352 x 3 96, 512 x 2 114; but 9,000 x 5,120: 128 x 5 68 us, 160 x 4 71).
+  const int most = p.nv <= 800 ? 5 : 4;
+  const int span = p.nv <= 8 ? 8 : 32 * ((p.nv + 32 * most - 1) / (32 * most));
   const int v = (p.nv + span - 1) / span;
   const int per_block = span <= 32 ? kWarpRowThreads / span : 1;
   const dim3 grid(static_cast<unsigned>((p.rows + per_block - 1) / per_block));
-  const cudaError_t e = span == 8    ? launch_pdl(norm_kernel<1, 8>, grid, dim3(kWarpRowThreads), 0, s, p)
-                        : span == 32 ? launch_norm<32>(v, grid, dim3(kWarpRowThreads), s, p)
-                                     : launch_norm<0>(v, grid, dim3(span), s, p);
-  return check_cuda(e, what);
+  return span == 8    ? launch_pdl(norm_kernel<1, 8, SUM>, grid, dim3(kWarpRowThreads), 0, s, p)
+         : span == 32 ? launch_norm<32, SUM>(v, grid, dim3(kWarpRowThreads), s, p)
+         : span <= kBlockRow ? launch_norm<kBlockRow, SUM>(v, grid, dim3(span), s, p)
+                             : launch_norm<kWideRow, SUM>(v, grid, dim3(span), s, p);
 }
 
 bool bad_rows(const void* a, int64_t ld, int32_t width) { return !aligned16(a) || ld % 8 || ld < width; }
@@ -262,7 +282,7 @@ extern "C" kalm_status kalm_rms_norm(const kalm_bf16* x, int64_t ldx, const kalm
   p.weight_offset = weight_offset;
   p.eps = eps;
   p.inv_width = 1.f / static_cast<float>(width);
-  return run_norm("launch norm_kernel (kalm_rms_norm)", p, static_cast<cudaStream_t>(stream));
+  return check_cuda(launch<false>(p, static_cast<cudaStream_t>(stream)), "launch norm_kernel (kalm_rms_norm)");
 }
 
 extern "C" kalm_status kalm_norm_residual(const kalm_bf16* y, int64_t ldy, const kalm_bf16* x, int64_t ldx,
@@ -310,5 +330,5 @@ extern "C" kalm_status kalm_norm_residual(const kalm_bf16* y, int64_t ldy, const
   p.weight_offset = weight_offset;
   p.eps = eps;
   p.inv_width = 1.f / static_cast<float>(width);
-  return run_norm("launch norm_kernel (kalm_norm_residual)", p, static_cast<cudaStream_t>(stream));
+  return check_cuda(launch<true>(p, static_cast<cudaStream_t>(stream)), "launch norm_kernel (kalm_norm_residual)");
 }

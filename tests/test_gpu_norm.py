@@ -179,3 +179,11 @@ def test_binding_refuses(kalm):
         with pytest.raises(kalm.KalmError):
             kalm.kalm_norm_residual(**(good | bad))
     assert kalm.kalm_check_device_errors() == 0
+
+
+@pytest.mark.parametrize("width", [64, 72, 512, 520, 1280, 1288, 2048, 5120, 6400, 6408, 8192, 12296, 16376])
+def test_widths_where_a_rows_threads_change(kalm, width):
+    """Rows of 8 lanes, of a warp, of a block of five and of four units a thread, on either side of each change."""
+    for case in [(([3, 0, 2], width, True, "doc", True, 0.5)), ([1, 9], width, True, "row", False, 1.0)]:
+        test_norm_residual(kalm, *case)
+    test_rms_norm(kalm, 6, width, 1.0)
