@@ -1,19 +1,21 @@
 // Merged attention over an 8-bit cache for a few decoder rows: a document's decoder positions times the query
 // heads of a KV head are at most KALM_CACHE_FEW_ROWS packed rows (one position with up to four heads a KV head, as in
-// a step that adds a token).  Same result as the tensor-core path of kalm_merged_attention_cache, one launch,
-// no workspace: there is too little arithmetic for tensor-core tiles (4 rows of 128 would be real).
+// a step that adds a token), or eight where the documents are short.  Same result as the tensor-core path of
+// kalm_merged_attention_cache, one launch, no workspace: there is too little arithmetic for tensor-core tiles (4 or
+// 8 rows of 128 would be real).
 //
 // Against the tensor-core path (us; one position per document, documents of 16 to 256 cached rows, one KV head):
 //   documents      1 row          2 rows         4 rows         8 rows
-//   1              5.1 / 12.0     6.2 / 12.0     8.2 / 12.0     11.8 / 12.0
-//   100            8.5 / 17.4     9.6 / 17.4     13.3 / 17.4    19.3 / 17.5
-//   1,000          45 / 112       52 / 112       77 / 112       115 / 112
-// so four rows are the border.  Bound by the latency of the dependent loads (offsets, pages, codes) for few
-// documents and by the fp32 pipe's instructions for many (100 documents: 6.9 MB in 13.3 us).
+//   1              5.1 / 12.0     6.0 / 12.0     8.2 / 12.0     12.7 / 12.0
+//   100            8.5 / 17.4     9.6 / 17.4     13.3 / 17.4    25.0 / 17.5
+//   1,000          45 / 112       52 / 112       77 / 112       88 / 112
+// so up to four rows always come here, five to eight where the documents are short or many (few_and_short).  Bound by the
+// latency of the dependent loads (offsets, pages, codes) for few
+// documents and by the fp32 pipe's instructions for many (100 documents of 4 rows: 6.9 MB in 13.3 us).
 //
-// One block per (document, KV head), eight warps.  For each packed row r and visible key j
+// One block per (document, KV head), eight warps (four of 8 rows each).  For each packed row r and visible key j
 //   s = scale * q_r . k_j;   out_r = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m)
-// A warp takes KEYS keys at a time (every eighth group of the document's), a lane 8 of the 256 columns of each:
+// A warp takes KEYS keys at a time (every eighth or fourth group of the document's), a lane 8 of the 256 columns of each:
 //   * the codes become fp32 numbers; their power-of-two scale multiplies the finished partial sum, not each number;
 //   * the KEYS x R partial dot products are summed over the lanes by halving: each exchange hands half of the sums
 //     to the other half of the lanes, so KEYS x R sums cost KEYS x R - 1 shuffles instead of five each, and a
@@ -34,7 +36,6 @@ namespace kalm {
 namespace {
 
 constexpr int kHeadDim = 256;
-constexpr int kWarps = 8;
 
 __device__ __forceinline__ void unpack_bf16x8(const uint4& v, F2 (&f)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -53,11 +54,12 @@ __device__ __forceinline__ void unpack_e4m3x8(const uint2& v, F2 (&f)[4]) {
 
 constexpr int log2_of(int n) { return n <= 1 ? 0 : 1 + log2_of(n / 2); }
 
-// R packed rows (1, 2 or 4), KEYS keys at a time; R * KEYS <= 32.  (4 keys at a time: 9.2, 10.6, 13.3 us for 1, 2, 4 rows of 100
-// documents against 8.4, 9.6, 13.1 then.)
+// R packed rows (1, 2, 4 or 8), KEYS keys at a time; R * KEYS <= 32.  (4 keys at a time: 9.2, 10.6, 13.3 us for 1, 2, 4 rows
+// of 100 documents against 8.4, 9.6, 13.1 then.)  8 rows' state takes the registers of four warps, their sums 32 KB.
 template <int R>
 struct Few {
-  static constexpr int KEYS = 8;
+  static constexpr int KEYS = R <= 4 ? 8 : 4;
+  static constexpr int WARPS = R <= 4 ? 8 : 4;
   static constexpr int N = R * KEYS;              // scores of a group of keys
   static constexpr int DUP = 5 - log2_of(N);      // the score of (key j, row r) is in lanes (j * R + r) << DUP and on
 };
@@ -75,7 +77,7 @@ struct State {
 template <int R>
 __device__ __forceinline__ void attend(State<R>& st, const F2 (&k)[Few<R>::KEYS][4], const float (&ks)[Few<R>::KEYS],
                                        const F2 (&v)[Few<R>::KEYS][4], const float (&vs)[Few<R>::KEYS], bool seen,
-                                       int lane, int G = 0) {
+                                       int lane, int G = 0, int j0 = 0) {
   constexpr int KEYS = Few<R>::KEYS, N = Few<R>::N, DUP = Few<R>::DUP;
   float part[N];
 #pragma unroll
@@ -130,7 +132,7 @@ __device__ __forceinline__ void attend(State<R>& st, const F2 (&k)[Few<R>::KEYS]
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const float pj = __shfl_sync(0xffffffffu, p, (j * R + r) << DUP) * vs[j];
-      if (j * G > r) continue;
+      if ((j0 + j) * G > r) continue;
 #pragma unroll
       for (int e = 0; e < 4; ++e) st.acc[r][e] = fma2(pair2(pj, pj), v[j][e], st.acc[r][e]);
     }
@@ -177,10 +179,10 @@ __device__ __forceinline__ void load_group(Group<R>& g, const CacheRowsParams& p
 }
 
 template <int R>
-__global__ void __launch_bounds__(kWarps * 32) cache_rows_attention_kernel(const CacheRowsParams p) {
+__global__ void __launch_bounds__(Few<R>::WARPS * 32) cache_rows_attention_kernel(const CacheRowsParams p) {
   pdl_launch_dependents();
   pdl_wait_predecessor();
-  constexpr int KEYS = Few<R>::KEYS, DUP = Few<R>::DUP;
+  constexpr int KEYS = Few<R>::KEYS, DUP = Few<R>::DUP, kWarps = Few<R>::WARPS;
   extern __shared__ float smem[];
   float* const acc_s = smem;                         // [kWarps][R][256]
   float* const m_s = smem + kWarps * R * kHeadDim;   // [kWarps][R]
@@ -227,22 +229,23 @@ __global__ void __launch_bounds__(kWarps * 32) cache_rows_attention_kernel(const
 
   // the last warp takes the self keys (at most R), the row's position and those before it
   if (warp == kWarps - 1) {
-    static_assert(KEYS >= KALM_CACHE_FEW_ROWS, "one group holds the self keys");
-    F2 k[KEYS][4], v[KEYS][4];
-    float one[KEYS];
+    for (int j0 = 0; j0 < (KEYS >= R ? 1 : static_cast<int>(lq)); j0 += KEYS) {  // (one group where KEYS >= R >= lq)
+      F2 k[KEYS][4], v[KEYS][4];
+      float one[KEYS];
 #pragma unroll
-    for (int j = 0; j < KEYS; ++j) {
-      uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-      if (j < static_cast<int>(lq)) {
-        const int64_t at = (in0 + j) * p.ld_self + static_cast<int64_t>(head) * kHeadDim + lane * 8;
-        a = *reinterpret_cast<const uint4*>(p.k_self + at);
-        b = *reinterpret_cast<const uint4*>(p.v_self + at);
+      for (int j = 0; j < KEYS; ++j) {
+        uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+        if (j0 + j < static_cast<int>(lq)) {
+          const int64_t at = (in0 + j0 + j) * p.ld_self + static_cast<int64_t>(head) * kHeadDim + lane * 8;
+          a = *reinterpret_cast<const uint4*>(p.k_self + at);
+          b = *reinterpret_cast<const uint4*>(p.v_self + at);
+        }
+        unpack_bf16x8(a, k[j]);
+        unpack_bf16x8(b, v[j]);
+        one[j] = 1.f;
       }
-      unpack_bf16x8(a, k[j]);
-      unpack_bf16x8(b, v[j]);
-      one[j] = 1.f;
+      attend<R>(st, k, one, v, one, my_row < rows && (j0 + my_key) * p.G <= my_row, lane, p.G, j0);
     }
-    attend<R>(st, k, one, v, one, my_row < rows && my_key * p.G <= my_row, lane, p.G);
   }
   while (next.n > 0) {
     const Group<R> cur = next;
@@ -279,7 +282,7 @@ __global__ void __launch_bounds__(kWarps * 32) cache_rows_attention_kernel(const
   __syncthreads();
   // join the warps: thread t has columns 2 (t % 128), rows t / 128, + 2, ...
   const int c2 = (threadIdx.x & 127) * 2;
-  for (int r = threadIdx.x >> 7; r < rows; r += 2) {
+  for (int r = threadIdx.x >> 7; r < rows; r += kWarps / 4) {
     float m = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) m = fmaxf(m, m_s[w * R + r]);
@@ -304,12 +307,12 @@ __global__ void __launch_bounds__(kWarps * 32) cache_rows_attention_kernel(const
 
 template <int R>
 constexpr int few_smem() {
-  return (kWarps * R * kHeadDim + 2 * kWarps * R) * static_cast<int>(sizeof(float));
+  return (Few<R>::WARPS * R * kHeadDim + 2 * Few<R>::WARPS * R) * static_cast<int>(sizeof(float));
 }
 
 template <int R>
 cudaError_t launch_rows(const CacheRowsParams& p, int n_docs, cudaStream_t s) {
-  return launch_pdl(cache_rows_attention_kernel<R>, dim3(static_cast<unsigned>(n_docs * p.n_kv)), dim3(kWarps * 32),
+  return launch_pdl(cache_rows_attention_kernel<R>, dim3(static_cast<unsigned>(n_docs * p.n_kv)), dim3(Few<R>::WARPS * 32),
                     few_smem<R>(), s, p);
 }
 
@@ -319,10 +322,11 @@ kalm_status launch_cache_rows_attention(const CacheRowsParams& p, int32_t n_docs
   const int rows = p.max_q * p.G;
   if (static_cast<int64_t>(n_docs) * p.n_kv > INT32_MAX)
     return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention_cache: too many work items");
-  static_assert(KALM_CACHE_FEW_ROWS == 4 && few_smem<4>() <= 48 * 1024, "row counts and shared memory");
+  static_assert(KALM_CACHE_FEW_ROWS == 4 && kCacheRowsMost == 8 && few_smem<4>() <= 48 * 1024 && few_smem<8>() <= 48 * 1024, "row counts and shared memory");
   return check_cuda(rows <= 1   ? launch_rows<1>(p, n_docs, stream)
                     : rows <= 2 ? launch_rows<2>(p, n_docs, stream)
-                                : launch_rows<4>(p, n_docs, stream),
+                    : rows <= 4 ? launch_rows<4>(p, n_docs, stream)
+                                : launch_rows<8>(p, n_docs, stream),
                     "launch cache_rows_attention_kernel");
 }
 

@@ -1394,6 +1394,18 @@ __global__ void __launch_bounds__(kWidenThreads) cache_widen_kernel(const WidenP
   }
 }
 
+// Whether the few-row form is the faster one for a call of KALM_CACHE_FEW_ROWS + 1 to kCacheRowsMost packed rows whose
+// documents have at most `places` cached rows (the table's; the lengths are on the device), with `items` blocks to
+// run.  5 to 8 rows, general / few-row form in us, documents of 1 .. places cached rows:
+//   places    1 item          148 items       200             400             1,000
+//   64        11.3 / 8.2      14.7 / 12.4     21.2 / 14.0     29.8 / 21.8     63.7 / 43.8
+//   128       11.3 / 9.5      16.1 / 17.0     24.2 / 19.9     35.6 / 29.1     83.7 / 62.1
+//   256       12.0 / 12.7     19.5 / 26.0     29.8 / 31.8     49.4 / 46.7     111 / 87.5
+bool few_and_short(int rows, int64_t places, int64_t items) {
+  const int sms = num_sms();
+  return rows <= kCacheRowsMost && (places <= 64 || (places <= 128 && items > sms) || (places <= 256 && items > 4 * sms));
+}
+
 }  // namespace
 }  // namespace kalm
 
@@ -1443,7 +1455,7 @@ extern "C" kalm_status kalm_merged_attention_cache(
   if (any && !few && n_docs > 65535)
     return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention_cache: n_docs=%d (at most 65,535)", n_docs);
   if ((st = ensure_device(nullptr)) != KALM_OK) return st;
-  if (any && few) {
+  if (any && (few || few_and_short(max_q * (n_q / n_kv), ld_table * page_rows, static_cast<int64_t>(n_docs) * n_kv))) {
     CacheRowsParams p{};
     p.q = reinterpret_cast<const __nv_bfloat16*>(q);
     p.k_self = reinterpret_cast<const __nv_bfloat16*>(k_self);

@@ -523,7 +523,9 @@ kalm_status kalm_cache_read(const uint8_t* codes, int64_t ld_codes, const uint8_
  * launches: the call's cached rows are widened to bf16 into the workspace, once for
  * all their query tiles, and attended over from there.  Calls of few rows (max_q *
  * n_q / n_kv <= KALM_CACHE_FEW_ROWS, as in a step of one position) are one launch
- * that reads the codes itself and neither needs nor touches the workspace.
+ * that reads the codes itself and neither needs nor touches the workspace.  Calls of
+ * up to twice as many rows take that launch too where the table's documents are
+ * short or many (the workspace is still asked for: it is the sizes that decide).
  *
  * q .. total_in, max_q, total_q, n_q .. lse   as kalm_merged_attention (order from
  *          kalm_attention_schedule for the same offsets and sizes, or NULL)

@@ -832,3 +832,50 @@ def test_few_rows_stay_inside_the_output(kalm):
         kalm.kalm_check_device_errors()
     got = from_dev(out)
     assert np.isfinite(got[:2]).all() and np.isnan(got[2]).all()
+
+
+@pytest.mark.parametrize("lq,nc,n_q,n_kv,page_rows", [
+    ([8, 7, 1, 0, 5, 8], [16, 0, 1, 15, 33, 64], 1, 1, 64),          # eight positions, self keys in two groups
+    ([2, 1, 2], [64, 3, 0], 4, 1, 32),
+    ([2, 2, 1, 0], [48, 17, 9, 5], 16, 4, 16),
+    ([1, 1], [13, 64], 8, 1, 8),
+    ([3], [40], 4, 2, 8),                                            # six rows of eight
+    ([8] * 150, [int(n) for n in np.arange(150) * 7 % 129], 1, 1, 128),   # many documents of two pages' length
+    ([2] * 160, [int(n) for n in np.arange(160) * 11 % 257], 16, 4, 256),
+])
+def test_short_documents(kalm, lq, nc, n_q, n_kv, page_rows):
+    """Five to eight rows over short or many documents take the few-row launch: nothing is rounded before its output."""
+    a = attention(np.random.default_rng(50 + n_q + len(lq)), lq, nc, n_q, n_kv, page_rows)
+    got, lse = run_attention(kalm, a, poison=True)
+    assert kalm.kalm_check_device_errors() == 0
+    want, want_lse, vmax = plain_attention(a)
+    check(got, lse, want, want_lse, vmax)
+    assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -15 * vmax[..., None]).all()
+    order = lambda q_off, p_off: _order(kalm, q_off, p_off, max(lq), n_q, n_kv)
+    last, _ = run_attention(kalm, a, order=None, last=True)
+    again, _ = run_attention(kalm, a, order=order)
+    np.testing.assert_array_equal(last, got)
+    np.testing.assert_array_equal(again, got)
+
+
+def _order(kalm, q_off, p_off, lq, n_q, n_kv):
+    out = torch.empty(kalm.kalm_attention_items(len(q_off) - 1, lq, n_q, n_kv), dtype=torch.int32, device="cuda")
+    kalm.kalm_attention_schedule(q_off, p_off, lq, n_q, n_kv, out)
+    return out
+
+
+def test_short_documents_do_not_see_later_values(kalm):
+    """Self keys in two groups: a NaN in row 5 of 8 stays out of rows 0 to 4 and reaches 5 to 7."""
+    a = attention(np.random.default_rng(60), [8], [20], 1, 1, 32)
+    want, want_lse, vmax = plain_attention(a)
+    a["vs"][5] = np.nan
+    got, lse = run_attention(kalm, a)
+    assert np.isnan(got[5:]).all()
+    check(got[:5], lse[:5], want[:5], want_lse[:5], vmax[:5])
+
+
+def test_group_sizes_that_do_not_divide_a_tile(kalm):
+    """Three query heads a KV head are refused in a call of few rows as in any other."""
+    a = attention(np.random.default_rng(61), [2], [40], 6, 2, 8)
+    with pytest.raises(kalm.KalmError, match="must divide 128"):
+        run_attention(kalm, a)
