@@ -336,7 +336,7 @@ def _cache_args(where: str, dev: int, row_off: torch.Tensor, page_table: torch.T
     if row_off.dtype is not torch.int64 or row_off.get_device() != dev or row_off.dim() != 1 or \
             not row_off.is_contiguous():
         _refuse(where, "offsets", row_off, torch.int64, dev, "expected a contiguous vector")
-    n_docs = len(row_off) - 1
+    n_docs = row_off.size(0) - 1
     if n_docs < 0:
         raise KalmError(1, where, "the offsets are empty")
     shape = page_table.shape
@@ -344,7 +344,7 @@ def _cache_args(where: str, dev: int, row_off: torch.Tensor, page_table: torch.T
             shape[0] != n_docs or not page_table.is_contiguous():
         _refuse(where, "page_table", page_table, torch.int32, dev, f"expected a contiguous [{n_docs}][pages] tensor")
     ld_codes = _mat(where, "codes", codes, torch.uint8, dev, -1, width)
-    cached = len(codes)
+    cached = codes.size(0)
     if page_rows <= 0 or cached % page_rows:
         raise KalmError(1, where, f"{cached} cache rows are not whole pages of {page_rows}")
     ld_scales = _mat(where, "scales", scales, torch.uint8, dev, cached, width // CACHE_GROUP)
@@ -408,7 +408,7 @@ def kalm_merged_attention_cache(q: torch.Tensor, k_self: torch.Tensor, v_self: t
     bf16 = torch.bfloat16
     max_q, page_rows = int(max_q), int(page_rows)
     dev = _device(where, q)
-    width, rows = n_kv * head_dim, len(q)
+    width, rows = n_kv * head_dim, q.size(0)
     n_docs, ld_table, n_pages, ld_codes, ld_scales = _cache_args(where, dev, pool_off, page_table, page_rows, k_codes,
                                                                  k_scales, width)
     ld_self = _mat(where, "k_self", k_self, bf16, dev, rows, width)
@@ -417,9 +417,10 @@ def kalm_merged_attention_cache(q: torch.Tensor, k_self: torch.Tensor, v_self: t
     _pair(where, "scales", k_scales, v_scales)
     ldq = _mat(where, "q", q, bf16, dev, rows, n_q * head_dim)
     ldo = _mat(where, "out", out, bf16, dev, -1, n_q * head_dim)
-    total_q = len(out) if total_q is None else int(total_q)
-    if total_q > len(out) or (in_off is None and total_q > rows):
-        raise KalmError(1, where, f"total_q={total_q} exceeds the rows of out ({len(out)}) or q ({rows})")
+    out_rows = out.size(0)
+    total_q = out_rows if total_q is None else int(total_q)
+    if total_q > out_rows or (in_off is None and total_q > rows):
+        raise KalmError(1, where, f"total_q={total_q} exceeds the rows of out ({out_rows}) or q ({rows})")
     if lse is not None and (lse.dtype is not torch.float32 or lse.get_device() != dev or lse.dim() != 2 or
                             lse.shape[0] < total_q or lse.shape[1] != n_q or not lse.is_contiguous()):
         _refuse(where, "lse", lse, torch.float32, dev, f"expected a contiguous [{total_q}][{n_q}] tensor")
@@ -440,7 +441,7 @@ def kalm_merged_attention_cache(q: torch.Tensor, k_self: torch.Tensor, v_self: t
     elif workspace is not None and _mat(where, "workspace", workspace, bf16, dev, -1, 2 * width) != 2 * width:
         raise KalmError(1, where, "the workspace must be contiguous")
     if workspace is not None:
-        ws, ws_rows = workspace.data_ptr(), len(workspace)
+        ws, ws_rows = workspace.data_ptr(), workspace.size(0)
     call(where, q.data_ptr(), ldq, k_self.data_ptr(), v_self.data_ptr(), ld_self, k_codes.data_ptr(),
          v_codes.data_ptr(), ld_codes, k_scales.data_ptr(), v_scales.data_ptr(), ld_scales, page_table.data_ptr(),
          ld_table, page_rows, n_pages, _vec(where, "q_off", q_off, torch.int64, dev, n_docs + 1),
