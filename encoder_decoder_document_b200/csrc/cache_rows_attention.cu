@@ -191,7 +191,11 @@ __global__ void __launch_bounds__(Few<R>::WARPS * 32) cache_rows_attention_kerne
   const int d = blockIdx.x / p.n_kv, head = blockIdx.x - d * p.n_kv;
   const int64_t q0 = __ldg(p.q_off + d), c0 = __ldg(p.pool_off + d);
   int64_t lq = __ldg(p.q_off + d + 1) - q0;
-  const int64_t nc = __ldg(p.pool_off + d + 1) - c0;
+  // Cached rows that the document claims, and those of them that its table has places for.  Only the latter are walked, so
+  // that wild offsets end in a flag and not in a loop of their length; the others, which count as rows of zeros (score 0,
+  // value 0), join the sums at the end.
+  const int64_t claimed = __ldg(p.pool_off + d + 1) - c0, places = p.pages.ld << p.pages.shift;
+  const int64_t nc = min(claimed, places);
   const int64_t in0 = p.in_off ? __ldg(p.in_off + d) : q0;
   if (lq <= 0) return;
   // more rows than the call was sized for, or rows (of q and self K / V, or of the output) that do not exist
@@ -199,6 +203,7 @@ __global__ void __launch_bounds__(Few<R>::WARPS * 32) cache_rows_attention_kerne
     if (threadIdx.x == 0) record_error(p.err, kErrDeviceArg | kSiteAttention);
     return;
   }
+  if ((claimed < 0 || claimed > places) && threadIdx.x == 0) record_error(p.err, kErrDeviceArg | kSiteAttention);
   const int rows = static_cast<int>(lq) * p.G;  // packed rows: position x head of the KV group
 
   // the first group's pages and codes go out before q is used
@@ -283,10 +288,10 @@ __global__ void __launch_bounds__(Few<R>::WARPS * 32) cache_rows_attention_kerne
   // join the warps: thread t has columns 2 (t % 128), rows t / 128, + 2, ...
   const int c2 = (threadIdx.x & 127) * 2;
   for (int r = threadIdx.x >> 7; r < rows; r += kWarps / 4) {
-    float m = -INFINITY;
+    float m = claimed > places ? 0.f : -INFINITY;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) m = fmaxf(m, m_s[w * R + r]);
-    float sum = 0.f, x = 0.f, y = 0.f;
+    float sum = claimed > places ? static_cast<float>(claimed - places) * ex2_approx(-m) : 0.f, x = 0.f, y = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float mw = m_s[w * R + r];
