@@ -539,8 +539,8 @@ kalm_status kalm_cache_read(const uint8_t* codes, int64_t ld_codes, const uint8_
  *          counts as 0 and is flagged.
  * workspace bf16 [workspace_rows][2 * n_kv * head_dim], 32-byte aligned, of at least
  *          kalm_merged_attention_cache_rows(pool_off[n_docs], n_docs) rows (a
- *          document that reaches past it is flagged); scratch, no contents are
- *          kept from call to call.  Calls that overlap on the GPU need their own.
+ *          document that reaches past it is flagged and attends to no cached row);
+ *          scratch, no contents are kept from call to call.  Calls that overlap on the GPU need their own.
  *          NULL with 0 rows where ld_table is 0 (nothing cached) or the rows are few.
  * Other documents' rows, self or cached, and what lies behind a document's last
  * row have no influence, NaN and infinities included.  Within a document, a NaN or

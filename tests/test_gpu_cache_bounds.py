@@ -63,3 +63,29 @@ def test_few_rows_of_a_negative_length(kalm):
     got, lse = run_attention(kalm, dict(a, p_off=np.array([0, 20, 10, 30])))
     assert flagged(kalm)
     check(got, lse, *want)
+
+
+@pytest.mark.parametrize("ws_rows,past", [(198, []), (197, [1]), (133, [1]), (127, [0, 1])])
+def test_documents_past_the_workspace(kalm, ws_rows, past):
+    """General form: a document whose widened rows do not fit the workspace is flagged and has no cached rows; the others
+    and the decoder rows' own attention are what they were."""
+    lq, nc = [40, 3], [70, 20]  # workspace rows 0 .. 127 (two tiles) and 134 .. 197
+    a = attention(np.random.default_rng(73), lq, nc, 4, 1, 16)
+    got, lse = run_attention(kalm, a, ws_rows=ws_rows)
+    if past:
+        assert flagged(kalm)
+    seen = dict(a, nc=[0 if d in past else n for d, n in enumerate(nc)])
+    check(got, lse, *plain_attention(seen))
+    assert kalm.kalm_check_device_errors() == 0
+
+
+def test_lengths_that_no_workspace_holds(kalm):
+    """General form: a negative length, and ones past 32 bits and past the workspace, are flagged and count as none."""
+    lq, nc = [33, 5, 40], [20, 30, 9]
+    a = attention(np.random.default_rng(74), lq, nc, 4, 1, 16)
+    for off, left in (([0, 20, 10, 19], [20, 0, 9]),             # document 1 ends before it starts
+                      ([0, 20, (1 << 32) + 50, 59], [20, 0, 0]),  # 2^32 + 30 rows, then a start past the workspace
+                      ([0, 20, 1 << 50, 1 << 50], [20, 0, 0])):
+        got, lse = run_attention(kalm, dict(a, p_off=np.array(off)), ws_rows=59 + 3 * 64)
+        assert flagged(kalm)
+        check(got, lse, *plain_attention(dict(a, nc=left)))
