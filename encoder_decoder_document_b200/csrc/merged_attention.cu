@@ -146,7 +146,7 @@ __device__ __forceinline__ Item make_item(const AttnParams& p, int w) {
   const int64_t nc = p.pool_off[it.d + 1] - it.c0;
   it.Nc = static_cast<int>(nc);
   if constexpr (CACHED) {
-    it.c0 += static_cast<int64_t>(it.d) * p.cross_pad;
+    it.c0 += static_cast<int64_t>(it.d) * p.cross_pad - p.pool_off[0];  // (the offsets may start anywhere)
     if (!widened_rows_fit(it.c0, nc, p.cross_rows)) it.Nc = 0;
   }
   it.pos0 = it.t * p.P;
@@ -1363,7 +1363,7 @@ __global__ void __launch_bounds__(kWidenThreads) cache_widen_kernel(const WidenP
   int32_t page = lane < p.warp_rows ? cache_page(p.pages, d, r0 + lane) : -1;
   const int64_t c0 = __ldg(p.pool_off + d);
   const int64_t nc = __ldg(p.pool_off + d + 1) - c0;
-  const int64_t to = c0 + static_cast<int64_t>(d) * kCrossPad;  // the document's first workspace row
+  const int64_t to = c0 - __ldg(p.pool_off) + static_cast<int64_t>(d) * kCrossPad;  // the document's first workspace row
   if (nc == 0) return;
   if (!widened_rows_fit(to, nc, p.ws_rows)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) record_error(p.err, kErrDeviceArg | kSiteAttention);

@@ -534,11 +534,11 @@ kalm_status kalm_cache_read(const uint8_t* codes, int64_t ld_codes, const uint8_
  * k_scales, v_scales their scale bytes: head g at byte g * 8, common stride
  *          ld_scales
  * pool_off int64[n_docs + 1]: document d attends to its first Nc[d] = pool_off[d+1]
- *          - pool_off[d] cached rows.  A row whose place in the table is missing or
+ *          - pool_off[d] cached rows; pool_off[0] may be any number.  A row whose place in the table is missing or
  *          names no page counts as a row of zeros and is flagged; a negative length
  *          counts as 0 and is flagged.
  * workspace bf16 [workspace_rows][2 * n_kv * head_dim], 32-byte aligned, of at least
- *          kalm_merged_attention_cache_rows(pool_off[n_docs], n_docs) rows (a
+ *          kalm_merged_attention_cache_rows(pool_off[n_docs] - pool_off[0], n_docs) rows (a
  *          document that reaches past it is flagged and attends to no cached row);
  *          scratch, no contents are kept from call to call.  Calls that overlap on the GPU need their own.
  *          NULL with 0 rows where ld_table is 0 (nothing cached) or the rows are few.

@@ -89,3 +89,18 @@ def test_lengths_that_no_workspace_holds(kalm):
         got, lse = run_attention(kalm, dict(a, p_off=np.array(off)), ws_rows=59 + 3 * 64)
         assert flagged(kalm)
         check(got, lse, *plain_attention(dict(a, nc=left)))
+
+
+@pytest.mark.parametrize("lq", [[40, 3, 130], [1, 1, 1], [2, 1, 2]])
+@pytest.mark.parametrize("start", [5, 1000, -7, 1 << 40])
+def test_offsets_that_start_elsewhere(kalm, lq, start):
+    """Only the differences of the cached rows' offsets count, in every form and with the workspace sized by them."""
+    nc = [70, 0, 20]
+    a = attention(np.random.default_rng(75), lq, nc, 4, 1, 16)
+    want = run_attention(kalm, a)
+    moved = dict(a, p_off=a["p_off"] + start)
+    for ws_rows in (None, kalm.kalm_merged_attention_cache_rows(90, 3)):
+        got = run_attention(kalm, moved, ws_rows=ws_rows)
+        np.testing.assert_array_equal(got[0], want[0])
+        np.testing.assert_array_equal(got[1], want[1])
+    assert kalm.kalm_check_device_errors() == 0
