@@ -29,7 +29,7 @@ __all__ = [
 HEAD_DIM = 256
 MAX_QUERY_TOKENS = 512  # KALM_MAX_QUERY_TOKENS
 CACHE_GROUP = 32  # KALM_CACHE_GROUP: columns of a cached row that share a scale
-CACHE_FEW_ROWS = 4  # KALM_CACHE_FEW_ROWS: packed rows up to which the cache attention takes no workspace
+CACHE_FEW_ROWS = 8  # KALM_CACHE_FEW_ROWS: packed rows up to which the cache attention takes no workspace
 
 
 # The current device and a device's current stream handle as torch keeps them, without the checks and the Stream

@@ -1,16 +1,23 @@
 // Merged attention over an 8-bit cache for a few decoder rows: a document's decoder positions times the query
-// heads of a KV head are at most KALM_CACHE_FEW_ROWS packed rows (one position with up to four heads a KV head, as in
-// a step that adds a token), or eight where the documents are short.  Same result as the tensor-core path of
-// kalm_merged_attention_cache, one launch, no workspace: there is too little arithmetic for tensor-core tiles (4 or
-// 8 rows of 128 would be real).
+// heads of a KV head are at most KALM_CACHE_FEW_ROWS packed rows (one position with up to eight heads a KV head, as in
+// a step that adds a token).  Same result as the tensor-core path of kalm_merged_attention_cache, one launch, no
+// workspace: there is too little arithmetic for tensor-core tiles (4 or 8 rows of 128 would be real).
 //
-// Against the tensor-core path (us; one position per document, documents of 16 to 256 cached rows, one KV head):
-//   documents      1 row          2 rows         4 rows         8 rows
-//   1              5.1 / 12.0     6.0 / 12.0     8.2 / 12.0     12.7 / 12.0
-//   100            8.5 / 17.4     9.6 / 17.4     13.3 / 17.4    25.0 / 17.5
-//   1,000          45 / 112       52 / 112       77 / 112       88 / 112
-// so up to four rows always come here, five to eight where the documents are short or many (few_and_short).  Bound by the
-// latency of the dependent loads (offsets, pages, codes) for few
+// Against the tensor-core path, this form / that one in us; one position per document, one KV head, documents of n / 16
+// to n cached rows:
+//   documents  rows    n = 64          256             512             1,024
+//   1          1       4.1 / 11.8      7.2 / 12.8      10.8 / 15.4     18.0 / 19.6
+//   1          4       6.1 / 11.8      10.8 / 13.0     16.4 / 15.4     27.1 / 20.0
+//   1          8       10.3 / 11.8     20.0 / 13.3     32.8 / 15.4     56.8 / 19.8
+//   100        1       4.6 / 14.4      8.7 / 18.0      14.3 / 24.2     25.1 / 39.7
+//   100        4       7.8 / 14.8      13.5 / 18.5     21.5 / 24.6     37.6 / 40.4
+//   100        8       12.4 / 14.9     25.6 / 18.5     44.3 / 24.9     82.5 / 40.4
+//   1,000      1       23.1 / 63.2     45.1 / 112      67.2 / 163      113 / 275
+//   1,000      4       40.9 / 64.6     76.5 / 113      111 / 164       179 / 279
+//   1,000      8       41.4 / 65.1     91.5 / 113      147 / 165       261 / 277
+// so it is the faster one but for long documents in small batches.  All calls of so few rows come here all the same:
+// the two forms round differently, and a choice by the documents' lengths or number would make a document's result
+// depend on its company.  Bound by the latency of the dependent loads (offsets, pages, codes) for few
 // documents and by the fp32 pipe's instructions for many (100 documents of 4 rows: 6.9 MB in 13.3 us).
 //
 // One block per (document, KV head), eight warps (four of 8 rows each).  For each packed row r and visible key j
@@ -327,7 +334,7 @@ kalm_status launch_cache_rows_attention(const CacheRowsParams& p, int32_t n_docs
   const int rows = p.max_q * p.G;
   if (static_cast<int64_t>(n_docs) * p.n_kv > INT32_MAX)
     return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention_cache: too many work items");
-  static_assert(KALM_CACHE_FEW_ROWS == 4 && kCacheRowsMost == 8 && few_smem<4>() <= 48 * 1024 && few_smem<8>() <= 48 * 1024, "row counts and shared memory");
+  static_assert(KALM_CACHE_FEW_ROWS == 8 && few_smem<4>() <= 48 * 1024 && few_smem<8>() <= 48 * 1024, "row counts and shared memory");
   return check_cuda(rows <= 1   ? launch_rows<1>(p, n_docs, stream)
                     : rows <= 2 ? launch_rows<2>(p, n_docs, stream)
                     : rows <= 4 ? launch_rows<4>(p, n_docs, stream)

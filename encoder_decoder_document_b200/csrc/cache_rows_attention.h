@@ -22,9 +22,7 @@ struct CacheRowsParams {
   uint32_t* err;
 };
 
-constexpr int kCacheRowsMost = 8;  // packed rows (max_q * G) of a launch, at most
-
-// Needs arguments that kalm_merged_attention_cache has checked.
+// Needs max_q * G <= KALM_CACHE_FEW_ROWS and arguments that kalm_merged_attention_cache has checked.
 kalm_status launch_cache_rows_attention(const CacheRowsParams& p, int32_t n_docs, cudaStream_t stream);
 
 }  // namespace kalm

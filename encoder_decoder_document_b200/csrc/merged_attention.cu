@@ -1415,18 +1415,6 @@ __global__ void __launch_bounds__(kWidenThreads) cache_widen_kernel(const WidenP
   }
 }
 
-// Whether the few-row form is the faster one for a call of KALM_CACHE_FEW_ROWS + 1 to kCacheRowsMost packed rows whose
-// documents have at most `places` cached rows (the table's; the lengths are on the device), with `items` blocks to
-// run.  5 to 8 rows, general / few-row form in us, documents of 1 .. places cached rows:
-//   places    1 item          148 items       200             400             1,000
-//   64        11.3 / 8.2      14.7 / 12.4     21.2 / 14.0     29.8 / 21.8     63.7 / 43.8
-//   128       11.3 / 9.5      16.1 / 17.0     24.2 / 19.9     35.6 / 29.1     83.7 / 62.1
-//   256       12.0 / 12.7     19.5 / 26.0     29.8 / 31.8     49.4 / 46.7     111 / 87.5
-bool few_and_short(int rows, int64_t places, int64_t items) {
-  const int sms = num_sms();
-  return rows <= kCacheRowsMost && (places <= 64 || (places <= 128 && items > sms) || (places <= 256 && items > 4 * sms));
-}
-
 }  // namespace
 }  // namespace kalm
 
@@ -1444,7 +1432,8 @@ extern "C" kalm_status kalm_merged_attention_cache(
     const int32_t* order, kalm_bf16* workspace, int64_t workspace_rows, kalm_bf16* out, int64_t ldo, float* lse,
     kalm_stream_t stream) {
   const int64_t width = static_cast<int64_t>(n_kv) * kD;
-  // few packed rows a KV head: no tensor-core tiles, no workspace
+  // Few packed rows a KV head: no tensor-core tiles, no workspace.  The rows that the call is sized for decide alone, so a
+  // document's result does not depend on the others in the call.
   const bool few = n_kv > 0 && n_q > 0 && n_q % n_kv == 0 && max_q >= 0 &&
                    static_cast<int64_t>(max_q) * (n_q / n_kv) <= KALM_CACHE_FEW_ROWS;
   const int64_t rows = few ? 0 : workspace_rows;
@@ -1476,7 +1465,7 @@ extern "C" kalm_status kalm_merged_attention_cache(
   if (any && !few && n_docs > 65535)
     return fail(KALM_ERR_INVALID_ARG, "kalm_merged_attention_cache: n_docs=%d (at most 65,535)", n_docs);
   if ((st = ensure_device(nullptr)) != KALM_OK) return st;
-  if (any && (few || few_and_short(max_q * (n_q / n_kv), ld_table * page_rows, static_cast<int64_t>(n_docs) * n_kv))) {
+  if (any && few) {
     CacheRowsParams p{};
     p.q = reinterpret_cast<const __nv_bfloat16*>(q);
     p.k_self = reinterpret_cast<const __nv_bfloat16*>(k_self);

@@ -485,7 +485,7 @@ kalm_status kalm_linear_rope(const kalm_bf16* x, int64_t ldx, const kalm_bf16* w
  * error word.
  * ------------------------------------------------------------------------- */
 #define KALM_CACHE_GROUP 32
-#define KALM_CACHE_FEW_ROWS 4
+#define KALM_CACHE_FEW_ROWS 8
 #define KALM_CACHE_MIN_PAGE_ROWS 8
 #define KALM_CACHE_MAX_PAGE_ROWS 1024
 
@@ -519,13 +519,13 @@ kalm_status kalm_cache_read(const uint8_t* codes, int64_t ld_codes, const uint8_
  * softmax over [causal self rows ; cross rows 0..Nc[d]-1], where document d's
  * cross rows are the rows of its pages.  The keys and values are the stored
  * numbers exactly, so the result is that of kalm_merged_attention over the rows
- * that kalm_cache_read returns.  Same passages as kalm_merged_attention.  Two
+ * that kalm_cache_read returns (bit for bit, but in calls of few rows, below, whose
+ * probabilities stay in fp32).  Same passages as kalm_merged_attention.  Two
  * launches: the call's cached rows are widened to bf16 into the workspace, once for
  * all their query tiles, and attended over from there.  Calls of few rows (max_q *
  * n_q / n_kv <= KALM_CACHE_FEW_ROWS, as in a step of one position) are one launch
- * that reads the codes itself and neither needs nor touches the workspace.  Calls of
- * up to twice as many rows take that launch too where the table's documents are
- * short or many (the workspace is still asked for: it is the sizes that decide).
+ * that reads the codes itself and neither needs nor touches the workspace.  max_q,
+ * n_q and n_kv alone decide, so a document's result is the same in any company.
  *
  * q .. total_in, max_q, total_q, n_q .. lse   as kalm_merged_attention (order from
  *          kalm_attention_schedule for the same offsets and sizes, or NULL)
@@ -534,13 +534,13 @@ kalm_status kalm_cache_read(const uint8_t* codes, int64_t ld_codes, const uint8_
  * k_scales, v_scales their scale bytes: head g at byte g * 8, common stride
  *          ld_scales
  * pool_off int64[n_docs + 1]: document d attends to its first Nc[d] = pool_off[d+1]
- *          - pool_off[d] cached rows; pool_off[0] may be any number.  A row whose place in the table is missing or
- *          names no page counts as a row of zeros and is flagged; a negative length
- *          counts as 0 and is flagged.
+ *          - pool_off[d] cached rows; pool_off[0] may be any number.  A row whose
+ *          place in the table is missing or names no page counts as a row of zeros
+ *          and is flagged; a negative length counts as 0 and is flagged.
  * workspace bf16 [workspace_rows][2 * n_kv * head_dim], 32-byte aligned, of at least
- *          kalm_merged_attention_cache_rows(pool_off[n_docs] - pool_off[0], n_docs) rows (a
- *          document that reaches past it is flagged and attends to no cached row);
- *          scratch, no contents are kept from call to call.  Calls that overlap on the GPU need their own.
+ *          kalm_merged_attention_cache_rows(pool_off[n_docs] - pool_off[0], n_docs)
+ *          rows (a document that reaches past it is flagged and attends to no cached
+ *          row); scratch, no contents are kept from call to call.  Calls that overlap on the GPU need their own.
  *          NULL with 0 rows where ld_table is 0 (nothing cached) or the rows are few.
  * Other documents' rows, self or cached, and what lies behind a document's last
  * row have no influence, NaN and infinities included.  Within a document, a NaN or

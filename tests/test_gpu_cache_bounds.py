@@ -104,3 +104,52 @@ def test_offsets_that_start_elsewhere(kalm, lq, start):
         np.testing.assert_array_equal(got[0], want[0])
         np.testing.assert_array_equal(got[1], want[1])
     assert kalm.kalm_check_device_errors() == 0
+
+
+@pytest.mark.parametrize("lq,n_q,n_kv", [(1, 4, 1), (2, 4, 1), (8, 1, 1), (3, 2, 1), (1, 8, 1), (2, 16, 4), (3, 4, 1), (40, 4, 1)])
+def test_a_document_in_any_company(kalm, lq, n_q, n_kv):
+    """A document's result, bit for bit: alone, beside one whose pages widen the table, and among many."""
+    rng = np.random.default_rng(76 + lq + n_q)
+    n = 300
+    a = attention(rng, [lq] * n, [40, 700] + [int(k) for k in rng.integers(0, 100, n - 2)], n_q, n_kv, 16)
+
+    def some(docs):
+        rows = np.concatenate([np.arange(a["q_off"][d], a["q_off"][d + 1]) for d in docs])
+        nc = [a["nc"][d] for d in docs]
+        width = max(1, max(-(-c // 16) for c in nc))
+        part = dict(a, lq=[lq] * len(docs), nc=nc, q_off=np.arange(len(docs) + 1) * lq, p_off=np.concatenate([[0], np.cumsum(nc)]),
+                    table=a["table"][list(docs), :width].copy(), q=a["q"][rows], ks=a["ks"][rows], vs=a["vs"][rows])
+        out, lse = run_attention(kalm, part)
+        return out.reshape(len(docs), lq, n_q, 256), lse.reshape(len(docs), lq, n_q)
+
+    alone = [some([d]) for d in (0, 1, 5)]
+    for docs in ([0, 1, 5], range(n)):
+        out, lse = some(list(docs))
+        for d, (o, l) in zip((0, 1, 5), alone):
+            np.testing.assert_array_equal(out[list(docs).index(d)], o[0])
+            np.testing.assert_array_equal(lse[list(docs).index(d)], l[0])
+    assert kalm.kalm_check_device_errors() == 0
+
+
+def test_a_cached_document_scores_alone_as_beside_a_long_one(kalm):
+    """Two decoder rows of four heads a KV head through the scorer: a short document's score, bit for bit."""
+    import synthetic
+    from encoder_decoder_document_b200.scorer import DeviceWeights, FBNLScorer
+    q = synthetic.make_query("tiny", layers=2, lq=2, doc_len=np.array([90, 1024, 7, 600]))
+    sc = FBNLScorer(DeviceWeights.from_bits(q.weights), q.n_q, q.n_kv)
+    cache = sc.new_cache(40, page_rows=16)
+    sc.cache_put(cache, range(4), q.enc, q.doc_len)
+    together = sc.score_rows_cached(q.x0, cache, [0, 1, 2, 3])
+    for d in range(4):
+        np.testing.assert_array_equal(sc.score_rows_cached(q.x0, cache, [d])[0], together[d])
+
+
+@pytest.mark.parametrize("lq,n_q,n_kv", [([2, 1], 4, 1), ([8, 5], 1, 1), ([1, 1], 8, 1)])
+def test_few_rows_take_no_workspace(kalm, lq, n_q, n_kv):
+    """Up to eight packed rows over documents of any length: nothing is rounded before the output, no workspace is needed."""
+    a = attention(np.random.default_rng(77), lq, [900, 33], n_q, n_kv, 64)
+    want, want_lse, vmax = plain_attention(a)
+    got, lse = run_attention(kalm, a, ws_rows=0)
+    check(got, lse, want, want_lse, vmax)
+    assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -15 * vmax[..., None]).all()
+    assert kalm.kalm_check_device_errors() == 0
