@@ -395,15 +395,18 @@ def kalm_merged_attention_cache(q: torch.Tensor, k_self: torch.Tensor, v_self: t
                                 lse: Optional[torch.Tensor] = None, head_dim: int = HEAD_DIM,
                                 in_off: Optional[torch.Tensor] = None, last_tile_only: bool = False,
                                 total_q: Optional[int] = None, order: Optional[torch.Tensor] = None,
-                                workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+                                workspace: Optional[torch.Tensor] = None, stream=None,
+                                total_pool: Optional[int] = None) -> None:
     """kalm_merged_attention with the cross K/V of an 8-bit document cache: document d attends to its
     first pool_off[d+1] - pool_off[d] cached rows.  k/v codes uint8 [cache rows][n_kv * head_dim]
     (column views of the cached rows are fine), k/v scales uint8 [cache rows][n_kv * head_dim / 32];
     the other arguments as kalm_merged_attention.
 
     workspace: bf16 scratch [>= kalm_merged_attention_cache_rows(cached rows, n_docs)][2 * n_kv * head_dim];
-    None allocates one for this call, for as many rows as the page table has places.  Calls of at most
-    CACHE_FEW_ROWS packed rows a KV head (max_q * n_q / n_kv) use none."""
+    None allocates one for this call: for `total_pool` cached rows (pool_off[-1] - pool_off[0], where the
+    caller has it on the host), or else for as many as the page table has places, which is far more where
+    one document is much longer than the rest.  Calls of at most CACHE_FEW_ROWS packed rows a KV head
+    (max_q * n_q / n_kv) use none."""
     where = "kalm_merged_attention_cache"
     bf16 = torch.bfloat16
     max_q, page_rows = int(max_q), int(page_rows)
@@ -432,7 +435,11 @@ def kalm_merged_attention_cache(q: torch.Tensor, k_self: torch.Tensor, v_self: t
             _refuse(where, "order", order, torch.int32, dev, f"expected at least the call's {items} work items")
     ws, ws_rows = None, 0
     if workspace is None and max_q * n_q > CACHE_FEW_ROWS * n_kv:
-        shape = (n_docs * (ld_table * page_rows + 64), 2 * width)  # every place of the table, see the rows helper below
+        if total_pool is None:
+            total_pool = n_docs * ld_table * page_rows  # every place of the table
+        elif total_pool < 0:
+            raise KalmError(1, where, f"total_pool={total_pool}")
+        shape = (total_pool + 64 * n_docs, 2 * width)  # kalm_merged_attention_cache_rows
         if stream is None:
             workspace = q.new_empty(shape)
         else:

@@ -5,6 +5,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+from tests.gpu_util import f64_to_dev, i32, i64
 from tests.test_gpu_cache import attention, check, plain_attention, run_attention
 
 pytestmark = pytest.mark.gpu
@@ -152,4 +153,37 @@ def test_few_rows_take_no_workspace(kalm, lq, n_q, n_kv):
     got, lse = run_attention(kalm, a, ws_rows=0)
     check(got, lse, want, want_lse, vmax)
     assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -15 * vmax[..., None]).all()
+    assert kalm.kalm_check_device_errors() == 0
+
+
+def test_the_default_workspace_of_uneven_documents(kalm):
+    """Told how many cached rows there are, the call allocates for those and not for every place of a wide page table."""
+    rng = np.random.default_rng(78)
+    n, lq = 200, 12
+    nc = [4000] + [int(k) for k in rng.integers(0, 30, n - 1)]
+    a = attention(rng, [lq] * n, nc, 4, 1, 64)
+    qkv = torch.cat([f64_to_dev(a[k].reshape(n * lq, -1)) for k in ("q", "ks", "vs")], 1)
+    codes, scales = torch.from_numpy(a["codes"]).cuda(), torch.from_numpy(a["scales"]).cuda()
+    out, ref = (torch.empty(n * lq, 1024, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    args = (qkv[:, :1024], qkv[:, 1024:1280], qkv[:, 1280:], codes[:, :256], scales[:, :8], codes[:, 256:], scales[:, 8:],
+            i32(a["table"]), 64, i64(a["q_off"]), i64(a["p_off"]), lq, 4, 1)
+
+    def peak(call):
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        call()
+        return torch.cuda.max_memory_allocated() - before
+
+    wide = peak(lambda: kalm.kalm_merged_attention_cache(*args, ref))
+    rows = kalm.kalm_merged_attention_cache_rows(sum(nc), n)
+    assert peak(lambda: kalm.kalm_merged_attention_cache(*args, out, total_pool=sum(nc))) <= rows * 1024 + (1 << 20) < wide // 20
+    assert torch.equal(out, ref)
+    with pytest.raises(kalm.KalmError):
+        kalm.kalm_merged_attention_cache(*args, out, total_pool=-1)
+    # calls of few rows allocate nothing
+    few = torch.empty(n, 2048, dtype=torch.bfloat16, device="cuda")
+    a8 = (torch.randn(n, 2048, device="cuda").bfloat16(), args[1][:n], args[2][:n], *args[3:9], i64(np.arange(n + 1)), args[10],
+          1, 8, 1)
+    assert peak(lambda: kalm.kalm_merged_attention_cache(*a8, few)) == 0
     assert kalm.kalm_check_device_errors() == 0
