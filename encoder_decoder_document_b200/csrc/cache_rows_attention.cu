@@ -204,9 +204,9 @@ __global__ void __launch_bounds__(Few<R>::WARPS * 32) cache_rows_attention_kerne
   const int64_t claimed = __ldg(p.pool_off + d + 1) - c0, places = p.pages.ld << p.pages.shift;
   const int64_t nc = min(claimed, places);
   const int64_t in0 = p.in_off ? __ldg(p.in_off + d) : q0;
-  if (lq <= 0) return;
+  if (lq == 0) return;
   // more rows than the call was sized for, or rows (of q and self K / V, or of the output) that do not exist
-  if (lq > p.max_q || in0 < 0 || in0 + lq > p.total_in || q0 < 0 || q0 + lq > p.total_q) {
+  if (lq < 0 || lq > p.max_q || in0 < 0 || in0 + lq > p.total_in || q0 < 0 || q0 + lq > p.total_q) {
     if (threadIdx.x == 0) record_error(p.err, kErrDeviceArg | kSiteAttention);
     return;
   }

@@ -96,6 +96,7 @@ struct AttnParams {
   int n_items;
   const int32_t* order;  // work items sorted heaviest first (kalm_attention_schedule); NULL: index order
   float scale_log2;  // scale * log2(e)
+  int total_q;       // rows of the output
   uint64_t wait_ns;
   uint32_t* err;
 };
@@ -130,7 +131,8 @@ __device__ __forceinline__ bool widened_rows_fit(int64_t to, int64_t nc, int row
 }
 
 // CACHED: the cross rows are widened ones of a workspace, cross_pad apart.  A document whose rows do not fit there
-// (flagged by the widening) has none, so that no offsets make a tile loop longer than the workspace.
+// (flagged by the widening) has none, so that no offsets make a tile loop longer than the workspace; one whose decoder
+// rows are not all the output's, or more than the call's tiles (flagged as well), is left out.
 template <bool CACHED>
 __device__ __forceinline__ Item make_item(const AttnParams& p, int w) {
   Item it;
@@ -139,7 +141,14 @@ __device__ __forceinline__ Item make_item(const AttnParams& p, int w) {
   it.g = rem % p.n_kv;
   it.d = rem / p.n_kv;
   it.q0 = p.q_off[it.d];
-  it.Lq = static_cast<int>(p.q_off[it.d + 1] - it.q0);
+  const int64_t lq = p.q_off[it.d + 1] - it.q0;
+  it.Lq = static_cast<int>(lq);
+  if constexpr (CACHED) {
+    const uint32_t high = static_cast<uint32_t>(it.q0 >> 32) | static_cast<uint32_t>(lq >> 32);
+    const uint32_t at = static_cast<uint32_t>(it.q0), end = static_cast<uint32_t>(p.total_q);
+    const uint32_t most = static_cast<uint32_t>(p.tiles_per_doc * p.P);
+    if (high || at > end || static_cast<uint32_t>(lq) > min(end - at, most)) it.Lq = 0;
+  }
   it.qi = p.in_off ? p.in_off[it.d] : it.q0;
   it.t = p.last_only ? (it.Lq > 0 ? (it.Lq - 1) / p.P : 0) : p.tiles_per_doc - 1 - w / per_t;
   it.c0 = p.pool_off[it.d];
@@ -1238,8 +1247,9 @@ kalm_status launch_attention(const kalm_bf16* q, int64_t ldq, const kalm_bf16* k
   prm.in_off = in_off;
   prm.last_only = last_tile_only ? 1 : 0;
   prm.pool_off = pool_off;
+  prm.total_q = static_cast<int>(total_q);  // (check_attention bounds both row counts)
   prm.cross_pad = cross_pad;
-  prm.cross_rows = static_cast<int>(total_pool);  // (check_attention bounds it)
+  prm.cross_rows = static_cast<int>(total_pool);
   prm.out = reinterpret_cast<__nv_bfloat16*>(out);
   prm.lse = lse;
   prm.ldo = ldo;
@@ -1349,6 +1359,9 @@ struct WidenParams {
   int ws_rows;
   int n_kv;
   int warp_rows;             // rows of a warp
+  const int64_t *q_off, *in_off;  // the documents' decoder rows, for their check
+  int64_t total_in, total_q;
+  int max_q;
   uint32_t* err;
 };
 
@@ -1364,6 +1377,12 @@ __global__ void __launch_bounds__(kWidenThreads) cache_widen_kernel(const WidenP
   const int64_t c0 = __ldg(p.pool_off + d);
   const int64_t nc = __ldg(p.pool_off + d + 1) - c0;
   const int64_t to = c0 - __ldg(p.pool_off) + static_cast<int64_t>(d) * kCrossPad;  // the document's first workspace row
+  if (blockIdx.x == 0 && threadIdx.x == kWidenThreads - 1) {
+    // decoder rows: more than the call was sized for, or rows (of the inputs, or of the output) that do not exist
+    const int64_t q0 = __ldg(p.q_off + d), lq = __ldg(p.q_off + d + 1) - q0, in0 = p.in_off ? __ldg(p.in_off + d) : q0;
+    if (lq < 0 || lq > p.max_q || (lq > 0 && (in0 < 0 || in0 + lq > p.total_in || q0 < 0 || q0 + lq > p.total_q)))
+      record_error(p.err, kErrDeviceArg | kSiteAttention);
+  }
   if (nc == 0) return;
   if (!widened_rows_fit(to, nc, p.ws_rows)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) record_error(p.err, kErrDeviceArg | kSiteAttention);
@@ -1505,7 +1524,7 @@ extern "C" kalm_status kalm_merged_attention_cache(
     const WidenParams wp{{k_codes, v_codes}, {k_scales, v_scales}, ld_codes, ld_scales,
                          CachePages{page_table, ld_table, n_pages, __builtin_ctz(static_cast<unsigned>(page_rows))},
                          pool_off, reinterpret_cast<__nv_bfloat16*>(workspace), static_cast<int>(rows), n_kv,
-                         warp_rows, device_error_word()};
+                         warp_rows, q_off, in_off, in_off ? total_in : total_q, total_q, max_q, device_error_word()};
     st = check_cuda(launch_pdl(cache_widen_kernel,
                                dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(n_docs)),
                                dim3(kWidenThreads), 0, static_cast<cudaStream_t>(stream), wp),

@@ -529,6 +529,8 @@ kalm_status kalm_cache_read(const uint8_t* codes, int64_t ld_codes, const uint8_
  *
  * q .. total_in, max_q, total_q, n_q .. lse   as kalm_merged_attention (order from
  *          kalm_attention_schedule for the same offsets and sizes, or NULL)
+ *          A document with more than max_q decoder rows, or with rows that are not in
+ *          the inputs or the output, is flagged; no row outside the output is written.
  * k_codes, v_codes  the cached K and V columns of this layer: head g of a row at
  *          byte g * 256; 16-byte aligned, common stride ld_codes
  * k_scales, v_scales their scale bytes: head g at byte g * 8, common stride

@@ -5,7 +5,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from tests.gpu_util import f64_to_dev, i32, i64
+from tests.gpu_util import f64_to_dev, from_dev, i32, i64
 from tests.test_gpu_cache import attention, check, plain_attention, run_attention
 
 pytestmark = pytest.mark.gpu
@@ -187,3 +187,38 @@ def test_the_default_workspace_of_uneven_documents(kalm):
           1, 8, 1)
     assert peak(lambda: kalm.kalm_merged_attention_cache(*a8, few)) == 0
     assert kalm.kalm_check_device_errors() == 0
+
+
+@pytest.mark.parametrize("q_off,total_q,in_off,skipped", [
+    ([0, 40, 43, 83], 50, None, [2]),                    # the last document's rows reach past the output's
+    ([0, 40, 1 << 40, 43], 83, None, [1, 2]),            # 2^40 rows, and a start past the output
+    ([0, 40, 43, 42], 83, None, [2]),                    # a document that ends before it starts
+    ([-5, 35, 38, 83], 83, None, [0]),                   # rows before the output; 45 rows of at most 40
+    ([0, 40, 43, 83], 43, [0, 40, 43], [2]),             # inputs that exist, an output that does not
+])
+def test_decoder_rows_outside_the_call(kalm, q_off, total_q, in_off, skipped):
+    """General form: flagged; nothing outside the output and nothing of another document is written."""
+    rng = np.random.default_rng(79)
+    a = attention(rng, [40, 3, 40], [70, 20, 5], 4, 1, 16)
+    qkv = torch.cat([f64_to_dev(a[k].reshape(83, -1)) for k in ("q", "ks", "vs")], 1)
+    codes, scales = torch.from_numpy(a["codes"]).cuda(), torch.from_numpy(a["scales"]).cuda()
+    whole = torch.full((300, 1024), 7.0, dtype=torch.bfloat16, device="cuda")  # the output, with rows on either side
+    out = whole[100:200]
+
+    kalm.kalm_merged_attention_cache(qkv[:, :1024], qkv[:, 1024:1280], qkv[:, 1280:], codes[:, :256], scales[:, :8],
+                                     codes[:, 256:], scales[:, 8:], i32(a["table"]), 16, i64(q_off), i64(a["p_off"]), 40, 4, 1,
+                                     out, total_q=total_q, in_off=None if in_off is None else i64(in_off))
+    assert flagged(kalm)
+    want, _, vmax = plain_attention(a)
+    got = from_dev(out).reshape(100, 4, 256)
+    written = np.zeros(100, bool)
+    for d in range(3):
+        if d not in skipped:
+            lo, hi = q_off[d], q_off[d + 1]
+            written[lo:hi] = True
+            src = slice(a["q_off"][d], a["q_off"][d + 1])
+            if (lo, hi) == (src.start, src.stop):
+                bound = 2.0 ** -8 * np.abs(want[src]) + (2.0 ** -8 + 2.0 ** -15) * vmax[src][..., None]
+                assert (np.abs(got[lo:hi] - want[src]) <= bound).all()
+    assert (got[~written] == 7.0).all()
+    assert bool((whole[:100] == 7.0).all()) and bool((whole[200:] == 7.0).all())
