@@ -14,6 +14,8 @@
 // on both sides and two neighbouring lanes hold one scale group; kUnits such slices per lane are loaded before the
 // first is used.  A warp's units are consecutive, so it searches the document of its first row once (128 offsets a
 // round) and walks on from there.
+#include <algorithm>
+
 #include "kalm.h"
 #include "kalm_cache.cuh"
 #include "kalm_internal.h"
@@ -60,6 +62,13 @@ struct Unit {
   int row, col;
   int64_t at;
 };
+
+// One thread of the launch flags documents whose packed rows are not all in memory; the others' are served.
+__device__ __forceinline__ void check_rows(const Rows& rows, uint32_t* err) {
+  if (blockIdx.x == 0 && threadIdx.x == kThreads - 1 &&
+      (__ldg(rows.off) < 0 || __ldg(rows.off + rows.n_docs) > rows.total))
+    record_error(err, kErrDeviceArg | kSiteCache);
+}
 
 // The warp's units and its first packed row.  Its rows are looked up once, a lane each: with units of 16 columns
 // and rows of at least two units a warp's 128 units are 64 rows at most (two a lane, and only where a row has two
@@ -150,6 +159,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const uint4* __re
                                                                uint32_t* err) {
   pdl_launch_dependents();
   pdl_wait_predecessor();
+  check_rows(rows, err);
   Unit u[kUnits];
   const uint4* const from = src + locate(u, rows, pages, err) * ld_src_v;
   Words8 x[kUnits];
@@ -217,6 +227,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const uint8_t* __r
                                                               uint32_t* err) {
   pdl_launch_dependents();
   pdl_wait_predecessor();
+  check_rows(rows, err);
   Unit u[kUnits];
   uint4* const to = dst + locate(u, rows, pages, err) * ld_dst_v;
   uint4 x[kUnits];
@@ -278,7 +289,7 @@ bool rows_aligned32(const void* p, int64_t ld) { return (reinterpret_cast<uintpt
 
 dim3 cache_grid(int64_t total_rows, int32_t width) {
   const int64_t units = total_rows * (width / kUnitCols);
-  return dim3(static_cast<unsigned>((units + kThreads * kUnits - 1) / (kThreads * kUnits)));
+  return dim3(static_cast<unsigned>(std::max((units + kThreads * kUnits - 1) / (kThreads * kUnits), int64_t{1})));  // (1: the rows' check)
 }
 
 }  // namespace
@@ -292,7 +303,7 @@ extern "C" kalm_status kalm_cache_write(const kalm_bf16* src, int64_t ld_src, co
                                     ld_table, page_rows, n_pages, codes, ld_codes, scales, ld_scales);
   if (st != KALM_OK) return st;
   if ((st = ensure_device(nullptr)) != KALM_OK) return st;
-  if (n_docs == 0 || total_rows == 0) return KALM_OK;
+  if (n_docs == 0 || (total_rows == 0 && !row_off)) return KALM_OK;
   return check_cuda(launch_pdl(rows_aligned32(src, ld_src) ? cache_write_kernel<true> : cache_write_kernel<false>, cache_grid(total_rows, width), dim3(kThreads), 0,
                                static_cast<cudaStream_t>(stream), reinterpret_cast<const uint4*>(src), ld_src / 8,
                                make_rows(row_off, first_row, n_docs, total_rows, width),
@@ -310,7 +321,7 @@ extern "C" kalm_status kalm_cache_read(const uint8_t* codes, int64_t ld_codes, c
                                     ld_table, page_rows, n_pages, codes, ld_codes, scales, ld_scales);
   if (st != KALM_OK) return st;
   if ((st = ensure_device(nullptr)) != KALM_OK) return st;
-  if (n_docs == 0 || total_rows == 0) return KALM_OK;
+  if (n_docs == 0 || (total_rows == 0 && !row_off)) return KALM_OK;
   return check_cuda(launch_pdl(rows_aligned32(dst, ld_dst) ? cache_read_kernel<true> : cache_read_kernel<false>, cache_grid(total_rows, width), dim3(kThreads), 0,
                                static_cast<cudaStream_t>(stream), codes, ld_codes, scales, ld_scales,
                                make_rows(row_off, first_row, n_docs, total_rows, width),

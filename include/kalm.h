@@ -492,7 +492,8 @@ kalm_status kalm_linear_rope(const kalm_bf16* x, int64_t ldx, const kalm_bf16* w
 /* Quantise packed rows into pages.
  * src      [total_rows][ld_src] bf16; document d's rows are row_off[d] ..
  *          row_off[d+1] - 1; rows that belong to no document are not read
- * row_off  int64[n_docs + 1], ascending
+ * row_off  int64[n_docs + 1], ascending, from 0 or more on; where it reaches past
+ *          total_rows the rows that do not exist are left out and flagged
  * first_row int32[n_docs] or NULL (zeros): src row row_off[d] + i becomes row
  *          first_row[d] + i of document d (rows appended to a cached document,
  *          down to a single one)

@@ -5,8 +5,8 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from tests.gpu_util import f64_to_dev, from_dev, i32, i64
-from tests.test_gpu_cache import attention, check, plain_attention, run_attention
+from tests.gpu_util import f64_to_dev, from_dev, i32, i64, rand_bf16
+from tests.test_gpu_cache import attention, check, dequantise, plain_attention, quantise, run_attention
 
 pytestmark = pytest.mark.gpu
 
@@ -222,3 +222,37 @@ def test_decoder_rows_outside_the_call(kalm, q_off, total_q, in_off, skipped):
                 assert (np.abs(got[lo:hi] - want[src]) <= bound).all()
     assert (got[~written] == 7.0).all()
     assert bool((whole[:100] == 7.0).all()) and bool((whole[200:] == 7.0).all())
+
+
+# ------------------------------------------------------------------ offsets past the rows in memory
+@pytest.mark.parametrize("rows,off", [(20, [0, 12, 25]), (20, [0, 20, 20, 21]), (20, [-3, 5, 20]), (0, [0, 4])])
+def test_write_and_read_of_rows_that_do_not_exist(kalm, rows, off):
+    """Documents whose offsets leave the tensor: the rows that exist are stored and read, the call is flagged."""
+    rng = np.random.default_rng(80)
+    v = rand_bf16(rng, (rows, 64))
+    src = f64_to_dev(v) if rows else torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    n = len(off) - 1
+    codes = torch.full((n * 32, 64), 0x55, dtype=torch.uint8, device="cuda")
+    scales = torch.full((n * 32, 2), 0x7F, dtype=torch.uint8, device="cuda")
+    table = i32(np.arange(n * 4).reshape(n, 4))
+    kalm.kalm_cache_write(src, i64(off), table, 8, codes, scales)
+    assert flagged(kalm)
+    want_c = np.full((n * 32, 64), 0x55, np.uint8)
+    c, _ = quantise(v) if rows else (None, None)
+    for d in range(n):
+        for r in range(max(off[d], 0), min(off[d + 1], rows)):
+            want_c[32 * d + r - off[d]] = c[r]
+    np.testing.assert_array_equal(codes.cpu().numpy(), want_c)
+    dst = torch.full((rows + 9, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    kalm.kalm_cache_read(codes, scales, i64(off), table, 8, dst[:rows])
+    assert flagged(kalm)
+    assert bool((dst[rows:] == 3.0).all())
+    in_doc = [r for r in range(rows) if any(a <= r < b for a, b in zip(off, off[1:]))]
+    stored = dequantise(want_c, scales.cpu().numpy())
+    for r in in_doc:
+        d = next(i for i in range(n) if off[i] <= r < off[i + 1])
+        np.testing.assert_array_equal(from_dev(dst[r:r + 1])[0], stored[32 * d + r - off[d]])
+    # offsets that end where the tensor does, or before, are as before
+    kalm.kalm_cache_write(src, i64([0] * n + [rows]), table, 8, codes, scales)
+    kalm.kalm_cache_write(src, i64([0] * n + [rows // 2]), table, 8, codes, scales)
+    assert kalm.kalm_check_device_errors() == 0
