@@ -88,7 +88,7 @@ kalm_status kalm_device_check(void);
  * *word_out (nullable) receives the raw word: bit 0 = a bounded wait expired,
  * bit 1 = invalid device data (e.g. a length above its limit); bits 8..15 name
  * the kernel (1 pool, 2 linear, 3 attention, 4 readout, 5 offsets, 6 self-test,
- * 7 rotary embedding, 8 document cache).
+ * 7 rotary embedding, 8 document cache, 9 norms).
  * Returns KALM_ERR_TIMEOUT, KALM_ERR_DEVICE_ARG or KALM_OK. */
 kalm_status kalm_check_device_errors(kalm_stream_t stream, uint32_t* word_out);
 
@@ -591,7 +591,8 @@ kalm_status kalm_rms_norm(const kalm_bf16* x, int64_t ldx, const kalm_bf16* w, k
  * gate     NULL: 1; with ld_gate = 0 one vector [width] for all rows; else
  *          [n_docs][ld_gate], document d's gate for rows q_off[d] .. q_off[d+1] - 1
  * q_off    int64[n_docs + 1] or NULL: with it, only the documents' rows are computed
- *          and the outputs' other rows keep their contents
+ *          and the outputs' other rows keep their contents; where it reaches outside
+ *          the `rows` rows, those that do not exist are left out and flagged
  * x_out    [rows][ldxo]; may be x or y (same stride)
  * w_pre, h [width] and [rows][ldh], or both NULL; h may be y (same stride, where
  *          x_out is not) */
