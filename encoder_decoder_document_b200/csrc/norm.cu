@@ -304,7 +304,7 @@ extern "C" kalm_status kalm_norm_residual(const kalm_bf16* y, int64_t ldy, const
   if (n_docs < 0 || ld_gate < 0) return fail(KALM_ERR_INVALID_ARG, "kalm_norm_residual: negative size");
   if (gate && ld_gate && !q_off)
     return fail(KALM_ERR_INVALID_ARG, "kalm_norm_residual: a gate per document needs q_off");
-  if ((h != nullptr) != (w_pre != nullptr))
+  if (rows > 0 && (h != nullptr) != (w_pre != nullptr))  // (without rows h may have no address)
     return fail(KALM_ERR_INVALID_ARG, "kalm_norm_residual: h and w_pre go together");
   const bool none = q_off ? n_docs == 0 : rows == 0;
   if (!none && rows > 0) {
