@@ -33,9 +33,10 @@ CACHE_FEW_ROWS = 8  # KALM_CACHE_FEW_ROWS: packed rows up to which the cache att
 
 
 # The current device and a device's current stream handle as torch keeps them, without the checks and the Stream
-# object around them (0.1 us instead of 3 us a call); called with a CUDA tensor in hand, so CUDA is initialised.
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
-_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# object around them (0.1 us instead of 3 us a call); called with a CUDA tensor in hand, so CUDA is initialised.  They
+# are torch's own, not public: where a version lacks one, the public call takes its place.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _stream(stream: Optional[torch.cuda.Stream], dev: Optional[int] = None) -> int:
