@@ -94,8 +94,9 @@ def _mat(where: str, name: str, t: torch.Tensor, dtype: torch.dtype, dev: int, r
 
 
 def _pair(where: str, name: str, k: torch.Tensor, v: torch.Tensor) -> None:
-    """The V tensor of a K / V pair is laid out as its (checked) K."""
-    if v.shape != k.shape or v.stride() != k.stride() or v.dtype is not k.dtype or v.get_device() != k.get_device():
+    """The V tensor of a K / V pair is laid out as its (checked) K (the stride of a single row is arbitrary in torch)."""
+    if v.shape != k.shape or v.dtype is not k.dtype or v.get_device() != k.get_device() or \
+            (v.stride() != k.stride() and (k.size(0) > 1 or v.stride(1) != 1)):
         raise KalmError(1, where, f"{name}: K is {k.dtype} {tuple(k.shape)} with strides {k.stride()} on {k.device}, V "
                                   f"{v.dtype} {tuple(v.shape)} with strides {v.stride()} on {v.device}")
 

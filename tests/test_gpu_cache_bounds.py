@@ -256,3 +256,21 @@ def test_write_and_read_of_rows_that_do_not_exist(kalm, rows, off):
     kalm.kalm_cache_write(src, i64([0] * n + [rows]), table, 8, codes, scales)
     kalm.kalm_cache_write(src, i64([0] * n + [rows // 2]), table, 8, codes, scales)
     assert kalm.kalm_check_device_errors() == 0
+
+
+# ------------------------------------------------------------------ a single row
+def test_one_row_of_any_stride(kalm):
+    """A single decoder row: the self K and V may be slices of one row or tensors of their own."""
+    a = attention(np.random.default_rng(81), [1], [20], 4, 1, 8)
+    want, want_lse = run_attention(kalm, a)
+    q, ks, vs = (f64_to_dev(a[k].reshape(1, -1)) for k in ("q", "ks", "vs"))
+    row = torch.cat([q, ks, vs, vs], 1)
+    codes, scales = torch.from_numpy(a["codes"]).cuda(), torch.from_numpy(a["scales"]).cuda()
+    out = torch.empty(1, 1024, dtype=torch.bfloat16, device="cuda")
+    for k, v in ((ks, vs), (row[:, 1024:1280], vs), (ks, row[:, 1536:]), (ks.expand(3, 256)[1:2], torch.stack([vs, vs], 1)[:, 1])):
+        kalm.kalm_merged_attention_cache(q, k, v, codes[:, :256], scales[:, :8], codes[:, 256:], scales[:, 8:], i32(a["table"]), 8,
+                                         i64([0, 1]), i64([0, 20]), 1, 4, 1, out.zero_())
+        np.testing.assert_array_equal(from_dev(out).reshape(want.shape), want)
+    with pytest.raises(kalm.KalmError):  # not a row of consecutive values
+        kalm.kalm_merged_attention_cache(q, ks, torch.cat([vs, vs], 1)[:, ::2], codes[:, :256], scales[:, :8], codes[:, 256:],
+                                         scales[:, 8:], i32(a["table"]), 8, i64([0, 1]), i64([0, 20]), 1, 4, 1, out)
