@@ -75,6 +75,12 @@ class DeviceWeights:
                    bf16_from_bits(w.w_no, device))
 
 
+# What prepare(), use_slot() and capture() keep of one query shape.
+_PREPARED = ("_shape", "n_docs", "total_tokens", "total_pooled", "lq", "slots", "slot", "enc", "doc_len", "x0", "tok_off",
+             "pool_off", "q_off", "zero_off", "one_doc_off", "pooled", "kv_cross", "qkv", "o", "x", "h", "y", "h0", "result",
+             "yes", "no", "margin", "score", "order", "sync", "chain_sync", "graph", "graphs", "graphs_decode", "graph_inst")
+
+
 class FBNLScorer:
     """Scores one query's documents.  With ``prune`` (the default) work that
     cannot reach the score is skipped, exactly: the first layer's Q/K/V are
@@ -115,6 +121,8 @@ class FBNLScorer:
         self.graph: Optional[torch.cuda.CUDAGraph] = None
         self.graphs = None
         self.graphs_decode = None
+        self.graph_inst = None
+        self._cached_set: dict = {}  # the buffers of queries over a DocumentCache, while this query's own are in place
         # optional per-launch timing: (label, event) recorded after every entry-point call
         self.marks: Optional[list] = None
         self.launches = 0  # kernel launches issued by the last forward()
@@ -170,6 +178,14 @@ class FBNLScorer:
         """Point the input buffers at slot i (for the next forward() or capture)."""
         self.slot = i
         self.enc, self.doc_len, self.x0 = (self.slots[i][k] for k in ("enc", "doc_len", "x0"))
+
+    def _exchange(self, other: dict) -> dict:
+        """Put another prepared set in place (empty: none yet) and return the one that was."""
+        mine = {k: self.__dict__.pop(k) for k in _PREPARED if k in self.__dict__}
+        if mine["graph_inst"] is not None:  # the marks are its events
+            mine["marks"], self.marks = self.marks, None
+        self.__dict__.update(dict(_shape=None, graph=None, graphs=None, graphs_decode=None, graph_inst=None) | other)
+        return mine
 
     # ------------------------------------------------------------------ steps
     def _mark(self, label: str) -> None:
@@ -651,7 +667,8 @@ class FBNLScorer:
 
     def score_rows_cached(self, x0: np.ndarray, cache: DocumentCache, keys) -> np.ndarray:
         """Rows (yes, no, margin, score) of cached documents for one query (``[len(keys)][4]`` float32 on
-        the host), in the order of ``keys``; x0: bf16 bits [lq][H]."""
+        the host), in the order of ``keys``; x0: bf16 bits [lq][H].  It has buffers of its own: what this scorer
+        prepared, captured or cached for its own documents stays as it is."""
         self._check_cache(cache)
         lq = int(np.asarray(x0).shape[0])
         if not 1 <= lq <= MAX_QUERY_TOKENS:
@@ -659,22 +676,24 @@ class FBNLScorer:
         if len(keys) == 0:
             return np.zeros((0, 4), dtype=np.float32)
         view = cache.view(keys)
-        self.prepare(len(keys), 0, 0, lq)
-        self.x0.copy_(bf16_from_bits(np.asarray(x0), cache.device))
-        items = kalm_attention_items(len(keys), lq, self.n_q, self.n_kv)
-        self.view_order = torch.empty(items, dtype=torch.int32, device=cache.device)
-        kalm_attention_schedule(self.q_off, view.row_off, lq, self.n_q, self.n_kv, self.view_order)
-        # one layer's cross K/V of these documents, widened; every layer uses the same scratch
-        self.view_ws = torch.empty(kalm_merged_attention_cache_rows(view.total_rows, len(keys)), 2 * self.n_kv * self.D,
-                                   dtype=torch.bfloat16, device=cache.device)
-        self.view_cache, self.view = cache, view
+        own = self._exchange(self._cached_set)
         try:
+            self.prepare(len(keys), 0, 0, lq)
+            self.x0.copy_(bf16_from_bits(np.asarray(x0), cache.device))
+            items = kalm_attention_items(len(keys), lq, self.n_q, self.n_kv)
+            self.view_order = torch.empty(items, dtype=torch.int32, device=cache.device)
+            kalm_attention_schedule(self.q_off, view.row_off, lq, self.n_q, self.n_kv, self.view_order)
+            # one layer's cross K/V of these documents, widened; every layer uses the same scratch
+            self.view_ws = torch.empty(kalm_merged_attention_cache_rows(view.total_rows, len(keys)),
+                                       2 * self.n_kv * self.D, dtype=torch.bfloat16, device=cache.device)
+            self.view_cache, self.view = cache, view
             self.launches = 0
             self.decode()
             res = self.scores_to_host().numpy()
             self.check_errors()
         finally:
             self.view = self.view_cache = self.view_ws = self.view_order = None
+            self._cached_set = self._exchange(own)
         return np.ascontiguousarray(res.T)
 
     def rerank_cached(self, x0: np.ndarray, cache: DocumentCache, keys, top_n: Optional[int] = None):

@@ -1,0 +1,111 @@
+"""Scoring from a document cache leaves what a scorer prepared, captured or cached for its own documents as it was."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import synthetic
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def kalm():
+    import __graft_entry__
+    __graft_entry__.build()
+    import encoder_decoder_document_b200 as k
+    k.kalm_device_check()
+    return k
+
+
+def pinned(bits):
+    return torch.from_numpy(np.ascontiguousarray(bits).view(np.int16)).view(torch.bfloat16).pin_memory()
+
+
+def scorer(q, **kw):
+    from encoder_decoder_document_b200.scorer import DeviceWeights, FBNLScorer
+    return FBNLScorer(DeviceWeights.from_bits(q.weights), q.n_q, q.n_kv, **kw)
+
+
+@pytest.mark.parametrize("instrument", [False, True])
+def test_graphs_and_cached_documents_survive(kalm, instrument):
+    """The prepared set, its captured graphs and the bf16 document cache, used before and after queries from a cache of
+    another number of documents and another query length."""
+    q = synthetic.make_query("tiny", layers=3)
+    other = synthetic.make_query("tiny", layers=3, lq=17)
+    sc = scorer(q)
+    plain = sc.score_rows(q.x0, q.enc, q.doc_len)
+    sc.capture(instrument=instrument)
+    kept = (sc.graph, list(sc.graphs), list(sc.graphs_decode), sc.graph_inst, sc.pool_off, sc.kv_cross, sc.result, sc._shape)
+    cache = sc.new_cache(16, page_rows=16)
+    sc.cache_put(cache, range(q.n_docs), q.enc, q.doc_len)
+    cached = [sc.score_rows_cached(other.x0, cache, [2, 0]), sc.score_rows_cached(q.x0, cache, [1]),
+              sc.score_rows_cached(other.x0, cache, [2, 0])]
+    np.testing.assert_array_equal(cached[0], cached[2])
+    assert (sc.graph, list(sc.graphs), list(sc.graphs_decode), sc.graph_inst, sc._shape) == (*kept[:4], kept[7])
+    assert sc.pool_off is kept[4] and sc.kv_cross is kept[5] and sc.result is kept[6]
+    np.testing.assert_array_equal(sc.scores_to_host().numpy().T, plain)  # the last query's scores are still there
+    # captured graphs
+    sc.result.zero_()
+    sc.run()
+    np.testing.assert_array_equal(sc.scores_to_host().numpy().T, plain)
+    outs = [torch.zeros(4, q.n_docs).pin_memory() for _ in range(3)]
+    sc.score_cached_stream([pinned(q.x0)] * 3, outs)
+    sc.check_errors()
+    for out in outs:
+        np.testing.assert_array_equal(out.numpy().T, plain)
+    if instrument:
+        n = len(sc.marks)
+        sc.graph_inst.replay()
+        torch.cuda.synchronize()
+        times = sc.kernel_times()
+        sc.score_rows_cached(q.x0, cache, [1])
+        assert len(sc.marks) == n and sorted(sc.kernel_times()) == sorted(times)
+        sc.marks = None
+    # eagerly: the query side over the documents of the last full forward, and a new capture
+    sc.result.zero_()
+    sc.forward(cached=True)
+    np.testing.assert_array_equal(sc.scores_to_host().numpy().T, plain)
+    sc.score_rows_cached(other.x0, cache, [2, 0])
+    sc.capture()
+    sc.score_rows_cached(other.x0, cache, [0])
+    sc.graphs_decode[0].replay()
+    np.testing.assert_array_equal(sc.scores_to_host().numpy().T, plain)
+    kalm.kalm_check_device_errors()
+
+
+def test_a_scorer_that_has_only_cached_documents(kalm):
+    """Nothing prepared before: cached queries work, and the scorer's own documents after them."""
+    q = synthetic.make_query("tiny", layers=2)
+    sc, ref = scorer(q), scorer(q)
+    cache = sc.new_cache(8, page_rows=32)
+    sc.cache_put(cache, range(q.n_docs), q.enc, q.doc_len)
+    first = sc.score_rows_cached(q.x0, cache, [0, 3])
+    assert sc._shape is None and sc.graph is None
+    with pytest.raises(KeyError):
+        sc.score_rows_cached(q.x0, cache, ["none"])
+    np.testing.assert_array_equal(sc.score_rows(q.x0, q.enc, q.doc_len), ref.score_rows(q.x0, q.enc, q.doc_len))
+    np.testing.assert_array_equal(sc.score_rows_cached(q.x0, cache, [0, 3]), first)
+
+
+def test_a_refused_query_changes_nothing(kalm, monkeypatch):
+    """An error in the middle of a cached query: the scorer's own set is in place again."""
+    q = synthetic.make_query("tiny", layers=2)
+    sc = scorer(q)
+    plain = sc.score_rows(q.x0, q.enc, q.doc_len)
+    cache = sc.new_cache(8, page_rows=32)
+    sc.cache_put(cache, range(q.n_docs), q.enc, q.doc_len)
+    good = sc.score_rows_cached(q.x0, cache, [1])
+
+    def refuse():
+        raise RuntimeError("refused")
+    monkeypatch.setattr(sc, "readout", refuse)
+    with pytest.raises(RuntimeError, match="refused"):
+        sc.score_rows_cached(q.x0, cache, [1, 2])
+    monkeypatch.undo()
+    assert sc.view is None
+    np.testing.assert_array_equal(sc.scores_to_host().numpy().T, plain)
+    sc.forward(cached=True)
+    np.testing.assert_array_equal(sc.scores_to_host().numpy().T, plain)
+    np.testing.assert_array_equal(sc.score_rows_cached(q.x0, cache, [1]), good)
+    kalm.kalm_check_device_errors()
