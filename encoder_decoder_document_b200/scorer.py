@@ -141,13 +141,14 @@ class FBNLScorer:
         rows = n_docs * lq
         kw = dict(device=device)
         self.n_docs, self.total_tokens, self.total_pooled, self.lq = shape
-        # two input slots, so the next query's inputs can be copied while this one runs
+        # two input slots, so the next query's inputs can be copied while this one runs; until then, and until their
+        # offsets are computed, the documents are empty (a step on memory's leftovers could walk any length)
         self.slots = [dict(enc=torch.empty(max(total_tokens, 1), H, dtype=torch.bfloat16, **kw),
-                           doc_len=torch.empty(n_docs, dtype=torch.int32, **kw),
-                           x0=torch.empty(lq, H, dtype=torch.bfloat16, **kw)) for _ in range(2)]
+                           doc_len=torch.zeros(n_docs, dtype=torch.int32, **kw),
+                           x0=torch.zeros(lq, H, dtype=torch.bfloat16, **kw)) for _ in range(2)]
         self.use_slot(0)
-        self.tok_off = torch.empty(n_docs + 1, dtype=torch.int64, **kw)
-        self.pool_off = torch.empty(n_docs + 1, dtype=torch.int64, **kw)
+        self.tok_off = torch.zeros(n_docs + 1, dtype=torch.int64, **kw)
+        self.pool_off = torch.zeros(n_docs + 1, dtype=torch.int64, **kw)
         # every document of a query has the query's Lq decoder rows, so their offsets belong
         # to the shape and are fixed here once (document d's rows start at d * Lq)
         self.q_off = torch.arange(n_docs + 1, dtype=torch.int64, **kw) * lq
@@ -163,9 +164,9 @@ class FBNLScorer:
             self.h0 = torch.empty(lq, H, dtype=torch.bfloat16, **kw)
         # (yes, no, margin, score) rows of one buffer: one device->host copy per query
         self.result = torch.empty(4, n_docs, dtype=torch.float32, **kw)
-        # work order of the full-layer attention launches (same costs in every layer)
-        self.order = torch.empty(max(kalm_attention_items(n_docs, lq, self.n_q, self.n_kv), 1), dtype=torch.int32,
-                                 **kw)
+        # work order of the full-layer attention launches (same costs in every layer); in index order until scheduled
+        self.order = torch.arange(max(kalm_attention_items(n_docs, lq, self.n_q, self.n_kv), 1), dtype=torch.int32,
+                                  **kw)
         self.yes, self.no, self.margin, self.score = self.result[0], self.result[1], self.result[2], self.result[3]
         # the fused layer's per-document counters (zero before a launch, left zero by it)
         self.sync = torch.zeros(max(kalm_attention_out_proj_sync_len(n_docs, lq, H), 1), dtype=torch.int32, **kw)

@@ -109,3 +109,26 @@ def test_a_refused_query_changes_nothing(kalm, monkeypatch):
     np.testing.assert_array_equal(sc.scores_to_host().numpy().T, plain)
     np.testing.assert_array_equal(sc.score_rows_cached(q.x0, cache, [1]), good)
     kalm.kalm_check_device_errors()
+
+
+def test_a_prepared_set_without_documents_yet(kalm):
+    """Between prepare() and the first documents a step or a capture sees empty documents, not memory's leftovers."""
+    q = synthetic.make_query("tiny", layers=2)
+    for _ in range(3):  # leave bytes in the allocator's blocks that offsets and lengths must not be made of
+        torch.full((1 << 20,), 0x7F, dtype=torch.uint8, device="cuda")
+    want = scorer(q).score_rows(q.x0, q.enc[:0], np.zeros(q.n_docs, dtype=np.int32))
+    sc = scorer(q)
+    sc.prepare(q.n_docs, int(q.doc_len.sum()), 500, q.x0.shape[0])
+    for t in (sc.slots[0]["doc_len"], sc.slots[1]["doc_len"], sc.pool_off, sc.tok_off):
+        assert int(t.abs().max()) == 0
+    assert sorted(sc.order.tolist()) == list(range(len(sc.order)))
+    sc.x0.copy_(pinned(q.x0))
+    sc.forward(cached=True)
+    np.testing.assert_array_equal(sc.scores_to_host().numpy().T, want)
+    kalm.kalm_check_device_errors()
+    sc.capture()
+    sc.run()
+    np.testing.assert_array_equal(sc.scores_to_host().numpy().T, want)
+    with pytest.raises(kalm.KalmError) as e:  # the pooling was promised 500 rows
+        sc.check_errors()
+    assert e.value.name == "KALM_ERR_DEVICE_ARG"
