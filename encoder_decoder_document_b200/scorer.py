@@ -135,7 +135,7 @@ class FBNLScorer:
         shape = (n_docs, total_tokens, total_pooled, lq)
         if self._shape == shape:
             return
-        self._shape = shape
+        self._shape = None  # until every buffer is there: a failed allocation leaves nothing half prepared
         self.graph = None
         D, H, L = self.D, self.H, self.L
         rows = n_docs * lq
@@ -174,6 +174,7 @@ class FBNLScorer:
         self.chain_sync = torch.zeros(max(kalm_linear_chain_sync_len(rows), 1), dtype=torch.int32, **kw)
         self.graphs = None
         self.graphs_decode = None
+        self._shape = shape
 
     def use_slot(self, i: int) -> None:
         """Point the input buffers at slot i (for the next forward() or capture)."""

@@ -132,3 +132,24 @@ def test_a_prepared_set_without_documents_yet(kalm):
     with pytest.raises(kalm.KalmError) as e:  # the pooling was promised 500 rows
         sc.check_errors()
     assert e.value.name == "KALM_ERR_DEVICE_ARG"
+
+
+@pytest.mark.parametrize("cached", [False, True])
+def test_an_allocation_that_fails_is_made_again(kalm, monkeypatch, cached):
+    """Out of memory in the middle of prepare(): the same query, asked again, gets its buffers."""
+    import encoder_decoder_document_b200.scorer as module
+    q = synthetic.make_query("tiny", layers=2)
+    sc = scorer(q)
+    cache = sc.new_cache(8, page_rows=32)
+    sc.cache_put(cache, range(q.n_docs), q.enc, q.doc_len)
+    ask = (lambda: sc.score_rows_cached(q.x0, cache, [0, 2])) if cached else (lambda: sc.score_rows(q.x0, q.enc, q.doc_len))
+
+    def refuse(*a, **k):
+        raise torch.cuda.OutOfMemoryError("no memory")
+    monkeypatch.setattr(module, "kalm_linear_chain_sync_len", refuse)
+    with pytest.raises(torch.cuda.OutOfMemoryError):
+        ask()
+    monkeypatch.undo()
+    ref = scorer(q)
+    want = ref.score_rows_cached(q.x0, cache, [0, 2]) if cached else ref.score_rows(q.x0, q.enc, q.doc_len)
+    np.testing.assert_array_equal(ask(), want)
