@@ -14,8 +14,9 @@
 // (121 -> 108 us at 26,077 x 2,560); a document's gate is asked for before the first sum, not after it (108 -> 90
 // us: it comes from L2, and its latency stood behind the sum's).
 // Measured (CUDA graph of calls over three sets of inputs; one gate for all / a gate per document): 12,800 x 640
-// 13.6 / 14.7 us = 4.5 TB/s; 25,600 x 1,152 39.8 / 42.0 us = 5.6 TB/s; 26,077 x 2,560 82.9 / 87.5 us = 6.1 TB/s (0.93 of
-// the copy bandwidth); 8,000 x 8,192 85.8 / 94.5 us = 5.5 TB/s; kalm_rms_norm of 26,077 x 2,560 40.8 us = 6.5 TB/s.
+// 15.1 / 16.9 us = 4.3 TB/s; 25,600 x 1,152 41.8 / 45.2 us = 5.6 TB/s; 26,077 x 2,560 85.6 / 95.4 us = 6.2 TB/s (0.95 of
+// the copy bandwidth); 8,000 x 8,192 89.0 / 99.4 us = 5.9 TB/s; kalm_rms_norm of 26,077 x 2,560 42.4 us = 6.3 TB/s.  (From
+// card to card these move by up to a tenth; the comparisons below are of one card each.)
 #include <algorithm>
 #include <cmath>
 

@@ -572,7 +572,8 @@ int64_t kalm_merged_attention_cache_rows(int64_t total_pool, int32_t n_docs);
  * are those of the base model's configuration; reading taken (the pages do not
  * spell them out): RMS norms, norm(v, w) = v / sqrt(mean(v^2) + eps) *
  * (w + weight_offset), with weight_offset 1 where a checkpoint stores w - 1.
- * fp32 from the loads to one rounding to bf16 per output.
+ * fp32 from the loads to one rounding to bf16 per output, the sums of squares too: a
+ * finite row whose sum passes 3.4e38 (values of 1e18 and more) is divided by infinity.
  * ------------------------------------------------------------------------- */
 #define KALM_NORM_MAX_WIDTH 16384
 
