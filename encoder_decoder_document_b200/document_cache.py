@@ -65,10 +65,18 @@ class DocumentCache:
     # ------------------------------------------------------------------ writing
     def put(self, keys: Sequence[Hashable], rows: Sequence[int], src: torch.Tensor) -> None:
         """New documents: ``src`` holds their rows packed one document after another (bf16 [sum(rows)][width])."""
+        self._check_new(keys)
+        self._write(keys, rows, src)
+
+    def check_put(self, keys: Sequence[Hashable], rows: Sequence[int]) -> None:
+        """Raise what ``put`` of these documents would raise for their keys, row counts and pages."""
+        self._check_new(keys)
+        self._plan(keys, rows)
+
+    def _check_new(self, keys) -> None:
         for k in keys:
             if k in self._docs:
                 raise KeyError(f"document {k!r} is cached already: drop it first, or append to it")
-        self._write(keys, rows, src)
 
     def append(self, keys: Sequence[Hashable], rows: Sequence[int], src: torch.Tensor) -> None:
         """More rows of cached documents (down to a single row), packed as for ``put``."""
@@ -77,18 +85,23 @@ class DocumentCache:
                 raise KeyError(f"document {k!r} is not cached")
         self._write(keys, rows, src)
 
-    def _write(self, keys, rows, src) -> None:
+    def _plan(self, keys, rows) -> tuple:
+        """(row counts, (pages, rows) held, new pages needed) of each document of a write."""
         rows = [int(r) for r in rows]
         if len(rows) != len(keys) or any(r < 0 for r in rows):
             raise ValueError(f"{len(keys)} documents, row counts {rows}")
         if len(set(keys)) != len(keys):
             raise ValueError("a document is named twice in one write")
-        if src.dim() != 2 or tuple(src.shape) != (sum(rows), self.width):
-            raise ValueError(f"src has shape {tuple(src.shape)}, expected ({sum(rows)}, {self.width})")
         old = [self._docs.get(k, ([], 0)) for k in keys]
         need = [-(-(o[1] + r) // self.page_rows) - len(o[0]) for o, r in zip(old, rows)]
         if sum(need) > len(self._free):
             raise MemoryError(f"the cache has {len(self._free)} free pages, {sum(need)} are needed")
+        return rows, old, need
+
+    def _write(self, keys, rows, src) -> None:
+        rows, old, need = self._plan(keys, rows)
+        if src.dim() != 2 or tuple(src.shape) != (sum(rows), self.width):
+            raise ValueError(f"src has shape {tuple(src.shape)}, expected ({sum(rows)}, {self.width})")
         taken = [self._free[len(self._free) - 1 - i] for i in range(sum(need))]
         pages, at = [], 0
         for o, n in zip(old, need):

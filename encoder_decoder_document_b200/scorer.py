@@ -75,6 +75,8 @@ class DeviceWeights:
                    bf16_from_bits(w.w_no, device))
 
 
+CACHE_PUT_BYTES = 1 << 30  # bf16 cross K/V that cache_put holds at a time
+
 # What prepare(), use_slot() and capture() keep of one query shape.
 _PREPARED = ("_shape", "n_docs", "total_tokens", "total_pooled", "lq", "slots", "slot", "enc", "doc_len", "x0", "tok_off",
              "pool_off", "q_off", "zero_off", "one_doc_off", "pooled", "kv_cross", "qkv", "o", "x", "h", "y", "h0", "result",
@@ -643,7 +645,8 @@ class FBNLScorer:
 
     def cache_put(self, cache: DocumentCache, keys, enc: np.ndarray, doc_len: np.ndarray) -> None:
         """Pool documents, project their cross K/V and store them under ``keys``; arguments as for
-        ``rerank`` (enc: bf16 bits of the documents' encoder states, packed)."""
+        ``rerank`` (enc: bf16 bits of the documents' encoder states, packed).  Documents go through in groups
+        whose cross K/V in bf16 take at most CACHE_PUT_BYTES; all of them are stored, or none."""
         self._check_cache(cache)
         doc_len = np.asarray(doc_len)
         if doc_len.ndim != 1 or len(keys) != doc_len.shape[0]:
@@ -651,21 +654,36 @@ class FBNLScorer:
         if doc_len.size and (doc_len.min() < 0 or doc_len.max() > MAX_DOC_TOKENS):
             raise ValueError(f"cache_put: document lengths must lie in [0, {MAX_DOC_TOKENS}]")
         doc_len = doc_len.astype(np.int32)
-        n, tokens = int(doc_len.shape[0]), int(doc_len.sum())
-        if np.asarray(enc).shape[0] < tokens:
-            raise ValueError(f"cache_put: enc holds {np.asarray(enc).shape[0]} rows, doc_len sums to {tokens}")
+        keys, enc, tokens = list(keys), np.asarray(enc), np.concatenate([[0], np.cumsum(doc_len, dtype=np.int64)])
+        if enc.shape[0] < tokens[-1]:
+            raise ValueError(f"cache_put: enc holds {enc.shape[0]} rows, doc_len sums to {tokens[-1]}")
         rows = ((doc_len.astype(np.int64) + self.chunk - 1) // self.chunk).tolist()
+        cache.check_put(keys, rows)
+        most, lo = CACHE_PUT_BYTES // (2 * cache.width), 0
+        try:
+            while lo < len(keys):
+                hi, total = lo + 1, rows[lo]
+                while hi < len(keys) and total + rows[hi] <= most:
+                    total += rows[hi]
+                    hi += 1
+                cache.put(keys[lo:hi], rows[lo:hi], self._document_rows(cache, enc[tokens[lo]:tokens[hi]], doc_len[lo:hi], total))
+                lo = hi
+        except BaseException:
+            cache.drop(keys[:lo])
+            raise
+
+    def _document_rows(self, cache: DocumentCache, enc: np.ndarray, doc_len: np.ndarray, total: int) -> torch.Tensor:
+        """What cache_put stores of some documents, in bf16: their ``total`` pooled vectors' cross K/V."""
         dev = cache.device
-        kv = torch.empty(sum(rows), cache.width, dtype=torch.bfloat16, device=dev)
-        if sum(rows):
-            states = bf16_from_bits(np.asarray(enc)[:tokens], dev)
+        kv = torch.empty(total, cache.width, dtype=torch.bfloat16, device=dev)
+        if total:
             lens = torch.from_numpy(doc_len).to(dev)
-            tok_off, pool_off = (torch.empty(n + 1, dtype=torch.int64, device=dev) for _ in range(2))
-            pooled = torch.empty(sum(rows), self.H, dtype=torch.bfloat16, device=dev)
+            tok_off, pool_off = (torch.empty(len(doc_len) + 1, dtype=torch.int64, device=dev) for _ in range(2))
+            pooled = torch.empty(total, self.H, dtype=torch.bfloat16, device=dev)
             kalm_ragged_offsets(lens, tok_off, pool_off, self.chunk)
-            kalm_chunk_pool(states, tok_off, lens, pooled, pool_off, sum(rows), self.chunk)
+            kalm_chunk_pool(bf16_from_bits(enc, dev), tok_off, lens, pooled, pool_off, total, self.chunk)
             kalm_cross_kv_proj(pooled, self.w.w_kv_cross, kv, self.n_kv, self.D)
-        cache.put(keys, rows, kv)
+        return kv
 
     def score_rows_cached(self, x0: np.ndarray, cache: DocumentCache, keys) -> np.ndarray:
         """Rows (yes, no, margin, score) of cached documents for one query (``[len(keys)][4]`` float32 on
