@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(Few<R>::WARPS * 32) cache_rows_attention_kerne
   const int64_t in0 = p.in_off ? __ldg(p.in_off + d) : q0;
   if (lq == 0) return;
   // more rows than the call was sized for, or rows (of q and self K / V, or of the output) that do not exist
-  if (lq < 0 || lq > p.max_q || in0 < 0 || in0 + lq > p.total_in || q0 < 0 || q0 + lq > p.total_q) {
+  if (lq < 0 || lq > p.max_q || in0 < 0 || in0 > p.total_in - lq || q0 < 0 || q0 > p.total_q - lq) {
     if (threadIdx.x == 0) record_error(p.err, kErrDeviceArg | kSiteAttention);
     return;
   }

@@ -1382,7 +1382,7 @@ __global__ void __launch_bounds__(kWidenThreads) cache_widen_kernel(const WidenP
   if (blockIdx.x == 0 && threadIdx.x == kWidenThreads - 1) {
     // decoder rows: more than the call was sized for, or rows (of the inputs, or of the output) that do not exist
     const int64_t q0 = __ldg(p.q_off + d), lq = __ldg(p.q_off + d + 1) - q0, in0 = p.in_off ? __ldg(p.in_off + d) : q0;
-    if (lq < 0 || lq > p.max_q || (lq > 0 && (in0 < 0 || in0 + lq > p.total_in || q0 < 0 || q0 + lq > p.total_q)))
+    if (lq < 0 || lq > p.max_q || (lq > 0 && (in0 < 0 || in0 > p.total_in - lq || q0 < 0 || q0 > p.total_q - lq)))
       record_error(p.err, kErrDeviceArg | kSiteAttention);
   }
   if (nc == 0) return;

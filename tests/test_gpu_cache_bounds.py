@@ -274,3 +274,15 @@ def test_one_row_of_any_stride(kalm):
     with pytest.raises(kalm.KalmError):  # not a row of consecutive values
         kalm.kalm_merged_attention_cache(q, ks, torch.cat([vs, vs], 1)[:, ::2], codes[:, :256], scales[:, :8], codes[:, 256:],
                                          scales[:, 8:], i32(a["table"]), 8, i64([0, 1]), i64([0, 20]), 1, 4, 1, out)
+
+
+@pytest.mark.parametrize("lq", [[1, 1], [40, 3]])
+@pytest.mark.parametrize("far", [(1 << 63) - 1, (1 << 63) - 40, -(1 << 63), 1 << 32])
+def test_input_rows_at_the_ends_of_64_bits(kalm, lq, far):
+    """First input rows so far out that adding a length to them would wrap: flagged, the other document as it was."""
+    a = attention(np.random.default_rng(82), lq, [9, 30], 4, 1, 16)
+    want, want_lse, vmax = plain_attention(a)
+    got, lse = run_attention(kalm, a, in_off=[0, far])
+    assert flagged(kalm)
+    n = lq[0]
+    check(got[:n], lse[:n], want[:n], want_lse[:n], vmax[:n])
