@@ -137,8 +137,8 @@ class FBNLScorer:
         shape = (n_docs, total_tokens, total_pooled, lq)
         if self._shape == shape:
             return
-        self._shape = None  # until every buffer is there: a failed allocation leaves nothing half prepared
-        self.graph = None
+        # until every buffer is there: a failed allocation leaves nothing half prepared, and no graph over freed buffers
+        self._shape = self.graph = self.graphs = self.graphs_decode = None
         D, H, L = self.D, self.H, self.L
         rows = n_docs * lq
         kw = dict(device=device)
@@ -174,8 +174,6 @@ class FBNLScorer:
         self.sync = torch.zeros(max(kalm_attention_out_proj_sync_len(n_docs, lq, H), 1), dtype=torch.int32, **kw)
         # the chained projections' per-row-block counters (zero before a launch, left zero by it)
         self.chain_sync = torch.zeros(max(kalm_linear_chain_sync_len(rows), 1), dtype=torch.int32, **kw)
-        self.graphs = None
-        self.graphs_decode = None
         self._shape = shape
 
     def use_slot(self, i: int) -> None:
@@ -408,6 +406,8 @@ class FBNLScorer:
         With ``cached`` only decode() runs: the documents' offsets, work order and
         cross K/V from the last full forward over the same documents are reused
         (the persistent-cache regime: one document set, many queries)."""
+        if self._shape is None:
+            raise RuntimeError("forward needs prepare() first")
         self.launches = 0
         if self.marks is not None:
             self._mark("start")

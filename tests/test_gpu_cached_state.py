@@ -153,3 +153,26 @@ def test_an_allocation_that_fails_is_made_again(kalm, monkeypatch, cached):
     ref = scorer(q)
     want = ref.score_rows_cached(q.x0, cache, [0, 2]) if cached else ref.score_rows(q.x0, q.enc, q.doc_len)
     np.testing.assert_array_equal(ask(), want)
+
+
+def test_a_failed_allocation_leaves_nothing_to_run(kalm, monkeypatch):
+    """After prepare() failed for another shape: no graph over the old buffers, no step over a mix of both."""
+    import encoder_decoder_document_b200.scorer as module
+    q = synthetic.make_query("tiny", layers=2)
+    sc = scorer(q)
+    plain = sc.score_rows(q.x0, q.enc, q.doc_len)
+    sc.capture()
+
+    def refuse(*a, **k):
+        raise torch.cuda.OutOfMemoryError("no memory")
+    monkeypatch.setattr(module, "kalm_attention_items", refuse)
+    with pytest.raises(torch.cuda.OutOfMemoryError):
+        sc.prepare(2 * q.n_docs, 1000, 250, q.x0.shape[0])
+    monkeypatch.undo()
+    for call in (sc.run, sc.forward, lambda: sc.forward(cached=True), sc.capture, lambda: sc.score_stream([], []),
+                 lambda: sc.score_cached_stream([], [])):
+        with pytest.raises(RuntimeError):
+            call()
+    np.testing.assert_array_equal(sc.score_rows(q.x0, q.enc, q.doc_len), plain)
+    with pytest.raises(RuntimeError):
+        scorer(q).forward()
